@@ -17,7 +17,8 @@
  * Tensor layout (all entry points): bf16, contiguous,
  *     q, o : [B, N, Hq,  D]      k, v : [B, N, Hkv, D]
  * Query head hq reads kv head hq / (Hq / Hkv) (consecutive q heads share a kv
- * head). D must be 64 or 128. RoPE, if any, is applied by the caller.
+ * head). D must be 64 or 128. Rotary positions are applied before
+ * (tm_rope_fwd).
  *
  * Numerics: scores and the softmax are fp32, the weights P bf16, and O, l fp32
  * sums on the tensor cores. The softmax reference (the running max) moves only
@@ -291,6 +292,189 @@ TM_API int tm_trianglemix_attn_fwd_noalloc(const void* q, const void* k, const v
                                            int B, int Hq, int Hkv, int N, int D, float scale,
                                            int S, int W, int L, int layer, int tri_start,
                                            void* stream);
+
+/*
+ * ---- Around the attention: positions, an 8-bit cache, and what it keeps ----
+ *
+ * A serving program rotates q and k by their positions (tm_rope_fwd), runs the
+ * prefill attention above, stores k and v in a paged 8-bit cache
+ * (tm_kv8_append) and from then on attends over that cache a few tokens at a
+ * time (tm_kv8_attn_fwd). When the cache has to shrink, it sums the attention
+ * weight that each key received (tm_key_weights_fwd from a prompt's last
+ * queries, the "last Q-K" rows that the triangle pattern keeps dense; or the
+ * weights output of tm_kv8_attn_fwd), chooses the keys to keep
+ * (tm_kv_select) and stores only those (tm_kv8_append with an index, straight
+ * from k and v) or moves them to fresh pages (tm_kv8_compact). The pages this
+ * library follows end with the prefill and have no counterpart.
+ *
+ * These calls follow the conventions at the top of this file (device pointers
+ * unless said otherwise, asynchronous on `stream`, no allocation, argument
+ * errors before anything is enqueued). lens, counts, kept, index and table
+ * contents are read on the device: values out of range are clamped or skipped
+ * as each call says and never lead to an access outside the buffers. Sizes that
+ * the caller declares (max_pages, num_pages, strides) must be those of the
+ * buffers. B and 2 * Hkv are at most 65535.
+ */
+
+/* Layouts of tm_rope_fwd: pairs (i, i + rot/2), or (2i, 2i + 1). */
+enum { TM_ROPE_HALF = 0, TM_ROPE_INTERLEAVED = 1 };
+
+/*
+ * Rotary positions. In every head of q [B, N, Hq, D] and k [B, N, Hkv, D] (bf16)
+ * the pair (a, b) number i < rot / 2 turns by t = pos * inv_freq[i]:
+ *   y_a = mscale (x_a cos t - x_b sin t),   y_b = mscale (x_b cos t + x_a sin t)
+ * and columns from rot on are copied. pos = positions[b * N + n] (int32, any
+ * value), or first + n where positions is NULL. inverse != 0 turns by -t (the
+ * transpose: it takes a rotation back when mscale is 1, and maps gradients).
+ * The angle is formed and reduced in fp64; the rotation is fp32, rounded to
+ * bf16 once.
+ *   inv_freq: rot / 2 doubles; tm_rope_inv_freq fills a host array with the
+ *     usual ones, frequencies stretched for long contexts among them.
+ *   rot: even, 2 .. D. Any D that is a multiple of 16, up to 512.
+ *   strides: elements between consecutive tokens, multiples of 8 and at least
+ *     heads * D, so that q and k may be read out of (or turned inside) a packed
+ *     q/k/v buffer; batches follow each other, N rows each.
+ *   q_out may be q itself and k_out k itself (same stride: in place), but no
+ *     output may otherwise overlap an input or the other output. k and k_out may
+ *     be NULL with Hkv = 0, q and q_out NULL with Hq = 0.
+ */
+TM_API int tm_rope_fwd(const void* q, void* q_out, const void* k, void* k_out, int B, int N, int Hq,
+                       int Hkv, int D, long long q_stride, long long q_out_stride,
+                       long long k_stride, long long k_out_stride, int rot, int layout, int inverse,
+                       const double* inv_freq, float mscale, const int* positions, long long first,
+                       void* stream);
+
+/*
+ * Rotary frequencies, into a HOST array of rot / 2 doubles:
+ *   f_i = base^(-2 i / rot),
+ * and for factor > 1 (a context `factor` times the one trained on) pairs that
+ * make fewer than low_turns turns over trained_len positions are slowed to
+ * f_i / factor, those that make more than high_turns stay, and those between
+ * are interpolated linearly in their number of turns:
+ *   s = clamp((trained_len f_i / 2 pi - low_turns) / (high_turns - low_turns), 0, 1),
+ *   f_i (s + (1 - s) / factor);
+ * with high_turns == low_turns, s is 1 above that number of turns and 0 up to
+ * it, so that low_turns = high_turns = HUGE_VAL slows every pair (position
+ * interpolation). Host only. base > 0, factor >= 1, trained_len >= 1, high_turns >= low_turns >= 0.
+ */
+TM_API int tm_rope_inv_freq(int rot, double base, double factor, double trained_len,
+                            double low_turns, double high_turns, double* out);
+
+/* Code formats of the 8-bit cache. */
+enum { TM_KV_INT8 = 0, TM_KV_E4M3 = 1 };
+
+/*
+ * The paged 8-bit cache.
+ *   k8, v8: codes [num_pages, Hkv, page, D], int8 or e4m3 (never 0x7F / 0xFF);
+ *   k_range, v_range: fp32 [num_pages, Hkv], >= 0. A code c of a (page, head)
+ *     block of range r stands for c * r / F, F = 127 (int8) or 448 (e4m3).
+ *   table: int32 [B, max_pages], the pages of each sequence in token order: its
+ *     token j is row j % page of page table[b, j / page]. Entries outside
+ *     [0, num_pages) are pages that are not there: their tokens are not
+ *     written, and read as absent.
+ *   page: 16, 32, 64 or 128. D: 64 or 128. k8 and v8 16-byte aligned.
+ * A page must not appear twice among the pages that one call writes.
+ *
+ * tm_kv8_append stores n tokens of k and v per sequence behind the lens[b] it
+ * holds (int32; clamped to the table's tokens). A block's range becomes the
+ * largest |x| stored in it: with a block that already holds tokens of the
+ * sequence, the larger of its range and the new tokens'; if that grows, the
+ * block's old codes move to it, each rounded once more. Codes are rounded to
+ * nearest, ties to even. The call neither changes lens nor reads ranges of
+ * blocks that held no token, and rows behind the last token keep their bytes.
+ *   k, v: bf16 [B, n_src, Hkv, D], k_stride / v_stride elements between tokens
+ *     (multiples of 8, at least Hkv * D), n_src tokens per sequence.
+ *   counts: int32 [B] or NULL: only the first counts[b] (clamped to [0, n]) of
+ *     the n tokens are stored. NULL: n.
+ *   index: int32 [B, Hkv, n] or NULL: token i of head h is row index[b, h, i]
+ *     of k and v (entries outside [0, n_src) store zeros). NULL: row i, and
+ *     n <= n_src.
+ * A block that receives a NaN or an infinity has that as its range and reads as
+ * NaN throughout. Tokens past the table's end are dropped.
+ */
+TM_API int tm_kv8_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                         int B, int n_src, int n, int Hkv, int D, const int* counts,
+                         const int* index, const int* lens, const int* table, int max_pages,
+                         void* k8, void* v8, float* k_range, float* v_range, int num_pages,
+                         int page, int format, void* stream);
+
+/*
+ * Attention of the last nq tokens of each sequence over the cache:
+ *   o[b, i, h] = sum_j softmax_j(scale q[b, i, h] . k_j) v_j,  j <= lens[b] - nq + i,
+ * with the cache's values for k and v (the nq tokens' own among them: append
+ * first). q, o: bf16 [B, nq, Hq, D]; Hq % Hkv == 0; nq >= 1. lens is clamped to
+ * [0, max_pages * page]; a row that sees no key is written as zeros. Scores,
+ * softmax and sums are fp32, the weights fp16 at a scale that keeps 11 bits of
+ * every weight above 2^-22 of the row's largest, K, V and q enter the products
+ * exactly.
+ *   weights: fp32 [B, Hkv, weights_stride] or NULL. The attention weight of key
+ *     j < lens[b], summed over the nq rows and the q heads of the group, is
+ *     stored at [b, h, j], or added to what is there if accumulate != 0.
+ *     weights_stride >= max_pages * page, or >= every lens[b] (keys at or past
+ *     weights_stride are not written).
+ *   workspace: 256-byte aligned, tm_kv8_attn_workspace_size bytes (host only);
+ *     calls that share one must be ordered.
+ * Results are the same from run to run. B <= 4096.
+ */
+TM_API int tm_kv8_attn_workspace_size(int B, int nq, int Hq, int Hkv, int D, int max_pages,
+                                      int page, int with_weights, long long* bytes);
+TM_API int tm_kv8_attn_fwd(const void* q, void* o, int B, int nq, int Hq, int Hkv, int D,
+                           float scale, const void* k8, const void* v8, const float* k_range,
+                           const float* v_range, int num_pages, int page, int format,
+                           const int* table, int max_pages, const int* lens, float* weights,
+                           long long weights_stride, int accumulate, void* workspace,
+                           long long workspace_bytes, void* stream);
+
+/*
+ * The attention weight that each key of a prompt receives from its last L
+ * queries, summed over them and the q heads of its group:
+ *   w[b, g, j] = sum_{i in [len - L, len), i >= j} sum_{h in g} softmax_j(scale q_ih . k_j)
+ * with causal rows; q [B, N, Hq, D], k [B, N, Hkv, D] as for tm_causal_attn_fwd.
+ * lens: int32 [B] or NULL: sequence b has lens[b] (clamped to [0, N]) tokens,
+ * the rows behind them are padding and neither read as keys nor written. L >= 1
+ * (L > len acts as len). weights: fp32 [B, Hkv, weights_stride >= N], stored for
+ * j < len, or added to if accumulate != 0. Hq / Hkv <= 128. workspace as above,
+ * of tm_key_weights_workspace_size bytes. Results are the same from run to run.
+ */
+TM_API int tm_key_weights_workspace_size(int B, int Hq, int Hkv, int N, int D, int L,
+                                         long long* bytes);
+TM_API int tm_key_weights_fwd(const void* q, const void* k, int B, int Hq, int Hkv, int N, int D,
+                              float scale, int L, const int* lens, float* weights,
+                              long long weights_stride, int accumulate, void* workspace,
+                              long long workspace_bytes, void* stream);
+
+/*
+ * The keys a cache keeps: of the lens[b] (NULL: n; clamped to [0, n]) tokens of
+ * each sequence and kv head, the first `sinks`, the last `recent`, and of the
+ * others those with the largest weights, min(lens[b], keep) in all; ties go to
+ * the lowest index, -0 equals 0, and NaN is below everything.
+ *   weights: fp32 [B, H, weights_stride >= n].
+ *   index: int32 [B, H, keep], ascending, -1 behind the kept ones.
+ *   kept: int32 [B] (may be NULL): min(lens[b], keep).
+ * sinks >= 0, recent >= 0, sinks + recent <= keep, keep >= 1, n >= 1.
+ */
+TM_API int tm_kv_select(const float* weights, long long weights_stride, const int* lens, int B,
+                        int H, int n, int keep, int sinks, int recent, int* index, int* kept,
+                        void* stream);
+
+/*
+ * Moves the chosen tokens of the cache to other pages, in order: token i <
+ * kept[b] (NULL: keep; clamped to [0, keep]) of head h becomes the old token
+ * index[b, h, i] of the same head, now at row i % page of page
+ * new_table[b, i / page]. A new block's range is the largest range of the old
+ * blocks its tokens come from, so codes from a block of that range move
+ * unchanged and others are rounded once more. Entries outside [0, lens[b]) or on
+ * pages that are not there store zeros. The pages of new_table must not be among
+ * those of table. weights (fp32 [B, Hkv, weights_stride], may be NULL with
+ * new_weights) move along: new_weights[b, h, i] = weights[b, h, index[b, h, i]].
+ * The caller then goes on with new_table and kept as its table and lens.
+ */
+TM_API int tm_kv8_compact(const int* index, int keep, const int* kept, const int* lens, int B,
+                          int Hkv, int D, const int* table, int max_pages, const int* new_table,
+                          int new_max_pages, void* k8, void* v8, float* k_range, float* v_range,
+                          int num_pages, int page, int format, const float* weights,
+                          long long weights_stride, float* new_weights,
+                          long long new_weights_stride, void* stream);
 
 /*
  * Number of kept (i, j) pairs of one (batch, head) of the triangle pattern:

@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libtm.so")
 
 TM_OK, TM_ERR_INVALID_ARG, TM_ERR_UNSUPPORTED, TM_ERR_CUDA, TM_ERR_TIMEOUT = 0, -1, -2, -3, -4
 TM_BLOCK_M = TM_BLOCK_N = 128
+TM_ROPE_HALF, TM_ROPE_INTERLEAVED = 0, 1
+TM_KV_INT8, TM_KV_E4M3 = 0, 1
 
 EXPORTED = (
     "tm_causal_attn_fwd", "tm_triangle_attn_fwd", "tm_trianglemix_attn_fwd",
@@ -33,6 +35,9 @@ EXPORTED = (
     "tm_trianglemix_sparse_attn_fwd", "tm_flashprefill_workspace_size",
     "tm_flashprefill_index_capacity", "tm_flashprefill_block_index", "tm_triangle_attn_fwd_heads",
     "tm_debug_inject_stall", "tm_debug_launch_count", "tm_debug_schedule_heads",
+    "tm_rope_fwd", "tm_rope_inv_freq", "tm_kv8_append", "tm_kv8_compact",
+    "tm_kv8_attn_workspace_size", "tm_kv8_attn_fwd", "tm_key_weights_workspace_size",
+    "tm_key_weights_fwd", "tm_kv_select",
 )
 
 
@@ -55,6 +60,7 @@ def lib() -> ctypes.CDLL:
                 "`python -m long_context_prefill_trianglemix_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, ci, cf, cll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
+        cd = ctypes.c_double
         sig = {
             "tm_causal_attn_fwd": (ci, [vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp]),
             "tm_triangle_attn_fwd": (ci, [vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, ci, ci, vp]),
@@ -98,6 +104,21 @@ def lib() -> ctypes.CDLL:
             "tm_debug_launch_count": (cll, []),
             "tm_debug_schedule_heads": (ci, [ci, ci, ci, ci, vp, vp, ci, ci, ci, vp, cll,
                                              ctypes.POINTER(cll)]),
+            "tm_rope_fwd": (ci, [vp, vp, vp, vp, ci, ci, ci, ci, ci, cll, cll, cll, cll, ci, ci,
+                                 ci, vp, cf, vp, cll, vp]),
+            "tm_rope_inv_freq": (ci, [ci, cd, cd, cd, cd, cd, vp]),
+            "tm_kv8_append": (ci, [vp, vp, cll, cll, ci, ci, ci, ci, ci, vp, vp, vp, vp, ci, vp,
+                                   vp, vp, vp, ci, ci, ci, vp]),
+            "tm_kv8_compact": (ci, [vp, ci, vp, vp, ci, ci, ci, vp, ci, vp, ci, vp, vp, vp, vp,
+                                    ci, ci, ci, vp, cll, vp, cll, vp]),
+            "tm_kv8_attn_workspace_size": (ci, [ci, ci, ci, ci, ci, ci, ci, ci,
+                                                ctypes.POINTER(cll)]),
+            "tm_kv8_attn_fwd": (ci, [vp, vp, ci, ci, ci, ci, ci, cf, vp, vp, vp, vp, ci, ci, ci,
+                                     vp, ci, vp, vp, cll, ci, vp, cll, vp]),
+            "tm_key_weights_workspace_size": (ci, [ci, ci, ci, ci, ci, ci, ctypes.POINTER(cll)]),
+            "tm_key_weights_fwd": (ci, [vp, vp, ci, ci, ci, ci, ci, cf, ci, vp, vp, cll, ci, vp,
+                                        cll, vp]),
+            "tm_kv_select": (ci, [vp, cll, vp, ci, ci, ci, ci, ci, ci, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -322,6 +343,80 @@ def tm_debug_schedule_heads(B, Hq, Hkv, N, S_heads, W_heads, L, num_ctas=148,
 def tm_debug_inject_stall(q, k, v, o, B, Hq, Hkv, N, D, scale, S, W, L, stream=None):
     return _check("tm_debug_inject_stall", lib().tm_debug_inject_stall(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, Hkv, N, D, scale, S, W, L, _stream(stream)))
+
+
+def tm_rope_fwd(q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_stride,
+                k_out_stride, rot, layout, inverse, inv_freq, mscale, positions, first,
+                stream=None):
+    return _check("tm_rope_fwd", lib().tm_rope_fwd(
+        _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), B, N, Hq, Hkv, D, q_stride, q_out_stride,
+        k_stride, k_out_stride, rot, layout, int(inverse), _ptr(inv_freq), mscale,
+        _ptr(positions), first, _stream(stream)))
+
+
+def tm_rope_inv_freq(rot, base, factor=1.0, trained_len=1.0, low_turns=0.0,
+                     high_turns=0.0) -> np.ndarray:
+    """The rotary frequencies (fp64, on the host), stretched by ``factor`` for long contexts."""
+    out = np.zeros(max(int(rot) // 2, 1), np.float64)
+    _check("tm_rope_inv_freq", lib().tm_rope_inv_freq(rot, base, factor, trained_len, low_turns,
+                                                      high_turns, out.ctypes.data))
+    return out
+
+
+def tm_kv8_append(k, v, k_stride, v_stride, B, n_src, n, Hkv, D, counts, index, lens, table,
+                  max_pages, k8, v8, k_range, v_range, num_pages, page, format, stream=None):
+    return _check("tm_kv8_append", lib().tm_kv8_append(
+        _ptr(k), _ptr(v), k_stride, v_stride, B, n_src, n, Hkv, D, _ptr(counts), _ptr(index),
+        _ptr(lens), _ptr(table), max_pages, _ptr(k8), _ptr(v8), _ptr(k_range), _ptr(v_range),
+        num_pages, page, format, _stream(stream)))
+
+
+def tm_kv8_compact(index, keep, kept, lens, B, Hkv, D, table, max_pages, new_table, new_max_pages,
+                   k8, v8, k_range, v_range, num_pages, page, format, weights, weights_stride,
+                   new_weights, new_weights_stride, stream=None):
+    return _check("tm_kv8_compact", lib().tm_kv8_compact(
+        _ptr(index), keep, _ptr(kept), _ptr(lens), B, Hkv, D, _ptr(table), max_pages,
+        _ptr(new_table), new_max_pages, _ptr(k8), _ptr(v8), _ptr(k_range), _ptr(v_range),
+        num_pages, page, format, _ptr(weights), weights_stride, _ptr(new_weights),
+        new_weights_stride, _stream(stream)))
+
+
+def tm_kv8_attn_workspace_size(B, nq, Hq, Hkv, D, max_pages, page, with_weights) -> int:
+    n = ctypes.c_longlong(0)
+    _check("tm_kv8_attn_workspace_size", lib().tm_kv8_attn_workspace_size(
+        B, nq, Hq, Hkv, D, max_pages, page, int(bool(with_weights)), ctypes.byref(n)))
+    return n.value
+
+
+def tm_kv8_attn_fwd(q, o, B, nq, Hq, Hkv, D, scale, k8, v8, k_range, v_range, num_pages, page,
+                    format, table, max_pages, lens, weights, weights_stride, accumulate,
+                    workspace, workspace_bytes, stream=None):
+    return _check("tm_kv8_attn_fwd", lib().tm_kv8_attn_fwd(
+        _ptr(q), _ptr(o), B, nq, Hq, Hkv, D, scale, _ptr(k8), _ptr(v8), _ptr(k_range),
+        _ptr(v_range), num_pages, page, format, _ptr(table), max_pages, _ptr(lens),
+        _ptr(weights), weights_stride, int(accumulate), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def tm_key_weights_workspace_size(B, Hq, Hkv, N, D, L) -> int:
+    n = ctypes.c_longlong(0)
+    _check("tm_key_weights_workspace_size", lib().tm_key_weights_workspace_size(
+        B, Hq, Hkv, N, D, L, ctypes.byref(n)))
+    return n.value
+
+
+def tm_key_weights_fwd(q, k, B, Hq, Hkv, N, D, scale, L, lens, weights, weights_stride,
+                       accumulate, workspace, workspace_bytes, stream=None):
+    return _check("tm_key_weights_fwd", lib().tm_key_weights_fwd(
+        _ptr(q), _ptr(k), B, Hq, Hkv, N, D, scale, L, _ptr(lens), _ptr(weights), weights_stride,
+        int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tm_kv_select(weights, weights_stride, lens, B, H, n, keep, sinks, recent, index, kept=None,
+                 stream=None):
+    return _check("tm_kv_select", lib().tm_kv_select(
+        _ptr(weights), weights_stride, _ptr(lens), B, H, n, keep, sinks, recent, _ptr(index),
+        _ptr(kept), _stream(stream)))
 
 
 def tm_get_device_status(stream=None) -> int:

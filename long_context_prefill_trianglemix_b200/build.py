@@ -75,7 +75,7 @@ def cuda_sources():
 def lib_inputs(extra=()):
     """(CUDA sources, every file the library depends on, nvcc flags)."""
     srcs = cuda_sources()
-    deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     flags = [*extra, *NVCC_ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
              "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
     return srcs, deps, flags

@@ -107,7 +107,8 @@ constexpr long long kSplitOverheadTiles = 1;
 // Where a wait gave up (recorded with the timeout, for diagnosis).
 enum WaitSite : int {
   kSiteQEmpty = 1, kSiteKvEmpty, kSiteQFull, kSiteKvFull, kSiteOEmpty, kSitePFull,
-  kSiteSFull, kSiteOFull, kSiteProbe, kSiteDisc, kSiteDescEmpty, kSiteDescFull
+  kSiteSFull, kSiteOFull, kSiteProbe, kSiteDisc, kSiteDescEmpty, kSiteDescFull,
+  kSiteWeights
 };
 
 template <int D>
@@ -1262,6 +1263,10 @@ __global__ void __launch_bounds__(128, 1)
 
 #include "tm_discover.cuh"
 
+// ------------------------------------------------------------------ key weights
+
+#include "tm_weights.cuh"
+
 // ------------------------------------------------------------------ host side
 
 namespace {
@@ -1282,6 +1287,7 @@ struct DeviceInfo {
   std::atomic<bool> attr_set[2] = {false, false};
   std::atomic<bool> probe_attr_set[2] = {false, false};
   std::atomic<bool> disc_attr_set[2] = {false, false};
+  std::atomic<bool> weights_attr_set[4] = {false, false, false, false};
 };
 
 constexpr int kMaxDevices = 64;
@@ -1665,7 +1671,94 @@ int launch_discovery_d(const DiscArgs& a, DeviceInfo* di) {
   return counted(5);
 }
 
+// Key weights: q tiles of tpt tokens of a group's q heads, and the workspace.
+struct WtLayout {
+  int tpt, nqt, nkt, splits;
+  long long lse, total;
+};
+WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
+  auto al = [](long long x) { return (x + 255) / 256 * 256; };
+  WtLayout l;
+  const int G = Hq / Hkv, rows = std::min(L, N);
+  l.tpt = 128 / G;
+  l.nqt = (rows + l.tpt - 1) / l.tpt;
+  l.nkt = (N + BN - 1) / BN;
+  // Pass 1 cuts the key range until there are about four items an SM, of four
+  // key tiles or more. The count is fixed so that a workspace's size is.
+  const long long pairs = static_cast<long long>(B) * Hkv * ((l.nqt + 1) / 2);
+  l.splits = static_cast<int>(
+      std::max(1LL, std::min<long long>((592 + pairs - 1) / pairs, (l.nkt + 3) / 4)));
+  const long long tile_rows = static_cast<long long>(B) * Hkv * l.nqt * 128;
+  l.lse = al(tile_rows * l.splits * 8);
+  l.total = l.lse + al(tile_rows * 4);
+  return l;
+}
+
+template <int D>
+int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
+  using C = WtCfg<D>;
+  const int kidx = D == 128 ? 1 : 0;
+  if (int rc = set_smem_once(di->weights_attr_set[kidx], weights_kernel<D, 1>, C::kSmem)) return rc;
+  if (int rc = set_smem_once(di->weights_attr_set[2 + kidx], weights_kernel<D, 2>, C::kSmem))
+    return rc;
+  const WtLayout l = weights_layout(a.B, a.Hq, a.Hkv, a.N, a.L);
+  if (a.ws_bytes < l.total) return TM_ERR_INVALID_ARG;
+  WtParams p;
+  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.N = a.N; p.G = a.Hq / a.Hkv; p.L = a.L;
+  p.tpt = l.tpt; p.nqt = l.nqt; p.nkt = l.nkt; p.splits = l.splits;
+  p.sl2 = a.scale * 1.4426950408889634f;
+  p.lens = a.lens;
+  p.stats = static_cast<float2*>(a.ws);
+  p.lse = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + l.lse);
+  p.weights = a.weights;
+  p.stride = a.stride;
+  p.accumulate = a.accumulate;
+  CUtensorMap tq, tk;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.N, (cuuint64_t)a.B};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2,
+                                 (cuuint64_t)a.N * a.Hq * D * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)p.G, (cuuint32_t)p.tpt, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  if (g_encode(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+          CUDA_SUCCESS ||
+      encode_bnhd(&tk, a.k, a.B, a.N, a.Hkv, D, BN))
+    return TM_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+  const long long bg = static_cast<long long>(a.B) * a.Hkv;
+  p.items = static_cast<int>(bg * ((l.nqt + 1) / 2) * l.splits);
+  weights_kernel<D, 1><<<std::min(p.items, di->sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
+  const long long rows = bg * l.nqt * 128;
+  weights_lse_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, st>>>(p);
+  p.items = static_cast<int>(bg * ((l.nkt + 1) / 2));
+  weights_kernel<D, 2><<<std::min(p.items, di->sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
+  return counted(3);
+}
+
 }  // namespace
+
+long long key_weights_workspace_bytes(int B, int Hq, int Hkv, int N, int D, int L) {
+  (void)D;
+  return weights_layout(B, Hq, Hkv, N, L).total;
+}
+
+int launch_key_weights(const KeyWeightsArgs& a) {
+  DeviceInfo* di = nullptr;
+  if (int rc = device_info(&di)) return rc;
+  if (a.D == 128) return launch_key_weights_d<128>(a, di);
+  if (a.D == 64) return launch_key_weights_d<64>(a, di);
+  return TM_ERR_UNSUPPORTED;
+}
+
+int device_sms(int* sms) {
+  DeviceInfo* di = nullptr;
+  if (int rc = device_info(&di)) return rc;
+  *sms = di->sms;
+  return TM_OK;
+}
+
+int count_launches(int n) { return counted(n); }
 
 long long kernel_launches() { return g_launches.load(std::memory_order_relaxed); }
 

@@ -45,6 +45,122 @@ struct DiscArgs {
   void* stream;
 };
 
+// Rotary positions (tm_rope.cu). Strides are elements between consecutive tokens.
+struct RopeArgs {
+  const void* q;
+  void* q_out;
+  const void* k;
+  void* k_out;
+  long long rows;  // B * N
+  int N, Hq, Hkv, D;
+  long long q_stride, q_out_stride, k_stride, k_out_stride;
+  int rot, layout, inverse;
+  const double* inv_freq;
+  float mscale;
+  const int* positions;
+  long long first;
+  void* stream;
+};
+
+// The paged 8-bit cache: codes [num_pages, Hkv, page, D], ranges [num_pages, Hkv].
+struct Kv8Cache {
+  void* k8;
+  void* v8;
+  float* k_range;
+  float* v_range;
+  int num_pages, page, format, Hkv, D;
+};
+
+struct Kv8AppendArgs {
+  Kv8Cache c;
+  const void* k;
+  const void* v;
+  long long k_stride, v_stride;
+  int B, n_src, n;
+  const int* counts;
+  const int* index;
+  const int* lens;
+  const int* table;
+  int max_pages;
+  void* stream;
+};
+
+struct Kv8CompactArgs {
+  Kv8Cache c;
+  const int* index;
+  int keep;
+  const int* kept;
+  const int* lens;
+  int B;
+  const int* table;
+  int max_pages;
+  const int* new_table;
+  int new_max_pages;
+  const float* weights;
+  long long weights_stride;
+  float* new_weights;
+  long long new_weights_stride;
+  void* stream;
+};
+
+struct Kv8AttnArgs {
+  Kv8Cache c;
+  const void* q;
+  void* o;
+  int B, nq, Hq;
+  float scale;
+  const int* table;
+  int max_pages;
+  const int* lens;
+  float* weights;
+  long long weights_stride;
+  int accumulate;
+  void* ws;
+  long long ws_bytes;
+  void* stream;
+};
+
+struct KvSelectArgs {
+  const float* weights;
+  long long stride;
+  const int* lens;
+  int B, H, n, keep, sinks, recent;
+  int* index;
+  int* kept;
+  void* stream;
+};
+
+struct KeyWeightsArgs {
+  const void* q;
+  const void* k;
+  int B, Hq, Hkv, N, D;
+  float scale;
+  int L;
+  const int* lens;
+  float* weights;
+  long long stride;
+  int accumulate;
+  void* ws;
+  long long ws_bytes;
+  void* stream;
+};
+
+// For the other translation units: the current device's SM count (TM_ERR_UNSUPPORTED
+// unless it is an sm_100), and the bookkeeping after n launches.
+int device_sms(int* sms);
+int count_launches(int n);
+
+int launch_rope(const RopeArgs& a);
+int launch_kv8_append(const Kv8AppendArgs& a);
+int launch_kv8_compact(const Kv8CompactArgs& a);
+int launch_kv8_attn(const Kv8AttnArgs& a);
+// Workspace of launch_kv8_attn on `sms` SMs.
+long long kv8_attn_workspace_bytes(int B, int nq, int Hq, int Hkv, int D, int max_pages, int page,
+                                   int with_weights);
+int launch_kv_select(const KvSelectArgs& a);
+int launch_key_weights(const KeyWeightsArgs& a);
+long long key_weights_workspace_bytes(int B, int Hq, int Hkv, int N, int D, int L);
+
 // All return a tm_status value.
 int launch_attention(const LaunchArgs& a);
 int launch_dump_tiles(const Pattern& p, int* out_dev, long long cap, void* stream);
