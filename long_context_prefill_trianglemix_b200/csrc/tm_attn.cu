@@ -38,6 +38,7 @@
 // are drained with bounded waits, TMEM is freed and the CTA exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,6 +50,7 @@
 
 #include "tm.h"
 #include "tm_internal.h"
+#include "tm_kv8.cuh"
 #include "tm_sm100.cuh"
 #include "tm_tiles.cuh"
 
@@ -108,7 +110,7 @@ constexpr long long kSplitOverheadTiles = 1;
 enum WaitSite : int {
   kSiteQEmpty = 1, kSiteKvEmpty, kSiteQFull, kSiteKvFull, kSiteOEmpty, kSitePFull,
   kSiteSFull, kSiteOFull, kSiteProbe, kSiteDisc, kSiteDescEmpty, kSiteDescFull,
-  kSiteWeights
+  kSiteWeights, kSiteKv8
 };
 
 template <int D>
@@ -1288,6 +1290,7 @@ struct DeviceInfo {
   std::atomic<bool> probe_attr_set[2] = {false, false};
   std::atomic<bool> disc_attr_set[2] = {false, false};
   std::atomic<bool> weights_attr_set[4] = {false, false, false, false};
+  std::atomic<bool> kv8_attr_set[8] = {};
 };
 
 constexpr int kMaxDevices = 64;
@@ -1872,5 +1875,9 @@ int read_and_clear_device_status(void* stream) {
   }
   return TM_OK;
 }
+
+// ------------------------------------------------------------------ attention over the 8-bit cache
+
+#include "tm_kv8_attn.cuh"
 
 }  // namespace trimix

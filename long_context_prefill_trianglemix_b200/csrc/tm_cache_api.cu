@@ -275,6 +275,7 @@ TM_API int tm_kv8_attn_fwd(const void* q, void* o, int B, int nq, int Hq, int Hk
   if (weights && (weights_stride < 1 || weights_stride > kIntMax)) return TM_ERR_INVALID_ARG;
   const long long qb = static_cast<long long>(B) * nq * Hq * D * 2;
   const long long pool = static_cast<long long>(num_pages) * Hkv * page * D;
+  if (pool / 64 > kIntMax) return TM_ERR_INVALID_ARG;  // rows of the pool in 32 bits
   const long long wb = static_cast<long long>(B) * Hkv * (weights ? weights_stride : 0) * 4;
   if (overlaps(o, qb, q, qb) || overlaps(o, qb, k8, pool) || overlaps(o, qb, v8, pool))
     return TM_ERR_INVALID_ARG;

@@ -1,0 +1,778 @@
+// Attention of a few query tokens per sequence over the paged 8-bit cache.
+//
+//   s_rj = scale q_r . k_j,  o_r = sum_j softmax_j(s_r)_j v_j,  j <= len - nq + i
+//
+// for the rows r = (query i, q head of the group) of a kv head. Reading the
+// codes once (2 D bytes a token and kv head) bounds it; everything else is
+// arranged so that the loads never wait for anything:
+//
+// - A unit is 16 tokens of one (page, head): 16 rows of D codes, contiguous. All
+//   units of all sequences and heads form one line, cut into equal parts for
+//   the CTAs and again for their warps, so ragged batches are balanced to a
+//   unit. A warp walks its part alone, across items, fed by its own ring of TMA
+//   loads (its lanes hold where the next 32 to 64 units lie).
+// - The codes are the A operand of m16n8k16 products and the (at most 8 NT) rows
+//   the n side, so a group of 4 or 8 q heads wastes no matrix work: S^T = K Q^T
+//   (16 tokens x 8 rows), O^T += V^T P^T (16 dims x 8 rows). The order of the
+//   contraction index is free, so each thread loads 16 contiguous bytes of its
+//   token rows and uses them in place; P^T goes from accumulator to operand
+//   layout by an 8x8 transpose (movmatrix).
+// - Codes become fp16 exactly (int8 by 1024 + u in the low mantissa bits, e4m3 by
+//   the conversion instruction). q becomes fp16 after an exact scaling of the
+//   row by a power of two that brings its largest element to [2^14, 2^15):
+//   fp16's 11 bits hold bf16's 8, and elements 2^-29 of the largest or less are
+//   rounded by at most 2^-40 of it. Products and sums are fp32.
+// - P is fp16, scaled by 2^8 against the running reference and allowed to grow
+//   to 2^15, which leaves weights down to 2^-32 of the largest in fp16's range
+//   (rounding 2^-12 of each weight, below the bf16 output's 2^-9). The
+//   reference moves only when a score exceeds it by more than 7 (log2), so the
+//   usual unit needs one vote and no rescale; m, l and O are fp32.
+//
+// Parts of an item (sequence, kv head, row tile) that end in one CTA are merged
+// there; an item cut between CTAs leaves unnormalised partials (O, m, l) in the
+// workspace and combine_kernel joins them in order, so results are reproducible.
+// Included by tm_attn.cu inside namespace trimix (status word, bounded waits, TMA
+// helpers, tensor-map encoding).
+
+namespace {
+
+using namespace kv8;
+
+constexpr int kAttnThreads = 256;
+constexpr int kAttnWarps = kAttnThreads / 32;
+constexpr int kUnit = 16;       // tokens
+constexpr int kMaxAttnBatch = 4096;
+constexpr int kMaxSms = 192;    // workspaces are sized for this many
+constexpr float kLift = 8.f;    // log2 of the scale of P against the reference
+constexpr float kSlack = 7.f;   // scores may exceed the reference by this
+constexpr float kLowest = -1.7e38f;
+
+struct AttnP {
+  Kv8AttnArgs a;
+  int G, rows, RT, items_per_b, page_log;
+  long long cap;      // tokens a sequence can hold
+  float* part_o;      // [2 grid][8 NT][D]
+  float2* part_ml;    // [2 grid][8 NT]
+  float* warp_o;      // [grid][warps][8 NT][D]: a warp's first partial
+  float* lse;         // [items][8 NT] (log2), +inf where a row keeps nothing
+  float* scores;      // [items][cap][8 NT] (log2), or null
+  int grid;
+};
+
+__device__ __forceinline__ int clamp_len(const AttnP& p, int b) {
+  return static_cast<int>(min(max(static_cast<long long>(p.a.lens[b]), 0LL), p.cap));
+}
+
+// How the line of T units is cut for `grid` CTAs: at least one unit a warp.
+__device__ __forceinline__ int parts_of(long long T, int grid) {
+  const long long most = (T + kAttnWarps - 1) / kAttnWarps;
+  return static_cast<int>(most < grid ? (most < 1 ? 1 : most) : grid);
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two f16 values of bytes 0, 1 (first) and 2, 3 (second) of a word of codes.
+template <int FMT>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& first, uint32_t& second) {
+  if (FMT == TM_KV_INT8) {
+    const uint32_t u = w ^ 0x80808080u;  // code + 128, 0..255
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 hx = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+    const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
+    first = *reinterpret_cast<const uint32_t*>(&hx);
+    second = *reinterpret_cast<const uint32_t*>(&hy);
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(first), "=r"(second)
+        : "r"(w));
+  }
+}
+
+// Shared memory of the kernel: each warp has a ring of S units (K rows, then V
+// rows, 128-byte swizzled by the TMA load).
+template <int D, int NT>
+struct AttnCfg {
+  static constexpr int S = (NT == 1 ? 3 : 6) * (D == 64 ? 2 : 1);
+  static constexpr int kHalf = kUnit * D;  // bytes of a unit's K or V
+  static constexpr int kWarpRing = S * 2 * kHalf;
+  static constexpr int kMl = kAttnWarps * kWarpRing;  // float2 [2 warps][8 NT]
+  static constexpr int kBar = kMl + 2 * kAttnWarps * 8 * NT * 8;
+  static constexpr int kItem = kBar + kAttnWarps * S * 8;
+  static constexpr int kPre = kItem + 2 * kAttnWarps * 4 + 16;  // int [B + 1]
+  static constexpr int kSmem = kPre + 16 + 1024;                // + 4 B, alignment slack
+  static_assert(8 * NT * D * 4 <= kWarpRing, "a partial must fit a warp's ring");
+};
+
+// Where one lane's unit of the line lies.
+struct UnitAt {
+  int item, u;
+  int row;  // TMA row of the unit, -1 if its page is not there
+  float kr, vr;
+};
+
+template <int D>
+__device__ __forceinline__ UnitAt locate(const AttnP& p, const int* pre, int x, int xe) {
+  UnitAt at;
+  at.item = -1; at.u = 0; at.row = -1;
+  at.kr = at.vr = 0.f;
+  if (x >= xe) return at;
+  int lo = 0, hi = p.a.B;  // the last b with pre[b] <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  const int U = (pre[lo + 1] - pre[lo]) / p.items_per_b;
+  const int it = (x - pre[lo]) / U;
+  at.u = x - pre[lo] - it * U;
+  at.item = lo * p.items_per_b + it;
+  const int tok0 = at.u * kUnit;
+  const int page = __ldg(p.a.table + static_cast<long long>(lo) * p.a.max_pages + (tok0 >> p.page_log));
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(p.a.c.num_pages)) {
+    const long long block = static_cast<long long>(page) * p.a.c.Hkv + it / p.RT;
+    at.row = static_cast<int>(((block << p.page_log) + (tok0 & (p.a.c.page - 1))) / (128 / D));
+    at.kr = __ldg(p.a.c.k_range + block);
+    at.vr = __ldg(p.a.c.v_range + block);
+  }
+  return at;
+}
+
+// Prefix sums of the sequences' units (times items per sequence) in shared memory.
+__device__ __forceinline__ void unit_prefix(const AttnP& p, int* pre) {
+  __shared__ int s_warp[kAttnWarps];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.a.B; b0 += kAttnThreads) {
+    const int b = b0 + t;
+    int x = b < p.a.B ? (clamp_len(p, b) + kUnit - 1) / kUnit * p.items_per_b : 0;
+    const int own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[w] = x;
+    __syncthreads();
+    int before = carry;
+    for (int i = 0; i < kAttnWarps; ++i) {
+      if (i < w) before += s_warp[i];
+      carry += s_warp[i];
+    }
+    if (b < p.a.B) pre[b] = before + x - own;
+    __syncthreads();
+  }
+  if (t == 0) pre[p.a.B] = carry;
+  __syncthreads();
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t* dst, float a, float b) {
+  *reinterpret_cast<uint32_t*>(dst) = sm100::pack_bf16x2(a, b);
+}
+
+template <int D>
+__device__ __forceinline__ uint16_t* out_row(const AttnP& p, int b, int h, int r) {
+  const int i = r / p.G;
+  return static_cast<uint16_t*>(p.a.o) +
+         ((static_cast<long long>(b) * p.a.nq + i) * p.a.Hq + h * p.G + (r - i * p.G)) * D;
+}
+
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
+    attn_kernel8(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                 const __grid_constant__ AttnP p) {
+  using C = AttnCfg<D, NT>;
+  constexpr int S = C::S;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kMl);
+  int* s_item = reinterpret_cast<int*>(smem + C::kItem);  // item of the slot's partial, or -1
+  volatile int* abort_flag = s_item + 2 * kAttnWarps;
+  int* pre = reinterpret_cast<int*>(smem + C::kPre);
+  const Kv8AttnArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar) + warp * S;
+  if (tid < 2 * kAttnWarps) s_item[tid] = -1;
+  if (tid == 0) {
+    *abort_flag = 0;
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (lane == 0)
+    for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
+  if (lane == 0) fence_barrier_init();
+  unit_prefix(p, pre);
+  const long long T = pre[a.B];
+  const int parts = parts_of(T, p.grid), cta = blockIdx.x;
+  if (cta >= parts) return;
+  const int cs = static_cast<int>(T * cta / parts), ce = static_cast<int>(T * (cta + 1) / parts);
+  const int xs = cs + static_cast<int>(static_cast<long long>(ce - cs) * warp / kAttnWarps);
+  const int xe = cs + static_cast<int>(static_cast<long long>(ce - cs) * (warp + 1) / kAttnWarps);
+  const int n_units = xe - xs;
+  const float s_unit = a.scale * 1.4426950408889634f / full<FMT>();
+  uint8_t* ring = smem + warp * C::kWarpRing;
+  const uint32_t ring_addr = smem_addr(ring);
+
+  // Lane i & 31 holds where unit i lies; the next 32 are looked up a batch ahead.
+  UnitAt cur = locate<D>(p, pre, xs + lane, xe), nxt = locate<D>(p, pre, xs + 32 + lane, xe);
+  auto issue = [&](int i, int batch) {
+    if (i >= n_units || lane != (i & 31)) return;
+    const int row = (i >> 5) == batch ? cur.row : nxt.row;
+    const int st = i % S;
+    uint64_t* bar = &bars[st];
+    if (row < 0) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_arrive_expect_tx(bar, 2 * C::kHalf);
+    tma_load_2d(ring_addr + st * 2 * C::kHalf, &tk, bar, 0, row);
+    tma_load_2d(ring_addr + st * 2 * C::kHalf + C::kHalf, &tv, bar, 0, row);
+  };
+  for (int i = 0; i < S - 1; ++i) issue(i, 0);
+
+  // Byte offsets of this thread's rows in a unit. K: tokens g and g + 8, 16-byte
+  // chunks 2t, 2t + 1 (D = 128) or t; V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, D / 8
+  // bytes at g D / 8. All but the 8-byte V loads of D = 64 are free of conflicts.
+  uint32_t k_off[2], v_off[4];
+  if (D == 128) {
+    k_off[0] = g * 128 + (((2 * t) ^ g) << 4);
+    k_off[1] = k_off[0] + 1024;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = 2 * t + (x & 1);
+      v_off[x] = C::kHalf + (r + 8 * (x >> 1)) * 128 + ((g ^ r) << 4);
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = (g >> 1) + 4 * x;
+      k_off[x] = r * 128 + ((((g & 1) * 4 + t) ^ r) << 4);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = t + 4 * (x >> 1);
+      v_off[x] = C::kHalf + r * 128 + ((((x & 1) * 4 + (g >> 1)) ^ r) << 4) + (g & 1) * 8;
+    }
+  }
+
+  int item = -1, b = 0, h = 0, row0 = 0, len = 0, u = 0, u_first = 0;
+  uint32_t qf[NT][D / 16][2];
+  float sc[NT][2], acc[NT][D / 16][4], ref[NT][2], l[NT][2];
+  int lim[NT][2];
+  float* scores = nullptr;
+  bool ok = true;
+
+  for (int i = 0; n_units > 0; ++i) {
+    if ((i & 31) == 0 && i > 0) {
+      cur = nxt;
+      nxt = locate<D>(p, pre, xs + i + 32 + lane, xe);
+    }
+    const int next_item = i < n_units ? __shfl_sync(0xffffffffu, cur.item, i & 31) : -1;
+    if (next_item != item) {
+      if (item >= 0) {
+        // ---- leave the item: its output, or this warp's partial of it
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+          }
+        if (u_first == 0 && u == (len + kUnit - 1) / kUnit) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int rr = row0 + 8 * n + 2 * t + e;
+              const bool some = l[n][e] != 0.f;
+              if (p.lse && g == 0)
+                p.lse[static_cast<long long>(item) * (8 * NT) + 8 * n + 2 * t + e] =
+                    some ? ref[n][e] - kLift + log2f(l[n][e]) : INFINITY;
+              if (rr >= p.rows) continue;
+              const float inv = some ? 1.f / l[n][e] : 0.f;
+              uint16_t* dst = out_row<D>(p, b, h, rr) + g * (D / 8);
+#pragma unroll
+              for (int m = 0; m < D / 16; ++m)
+                store_bf16(dst + 2 * m, acc[n][m][e] * inv, acc[n][m][e + 2] * inv);
+            }
+        } else {
+          // slot 0 (more items follow, the ring is in use): global scratch; slot 1 (the
+          // warp's last item, all its units consumed): the ring
+          const int slot = 2 * warp + (i == n_units);
+          float* o = i == n_units
+                         ? reinterpret_cast<float*>(ring)
+                         : p.warp_o + (static_cast<long long>(cta) * kAttnWarps + warp) * 8 * NT * D;
+          if (lane == 0) s_item[slot] = item;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 8 * n + 2 * t + e;
+              if (g == 0) s_ml[slot * 8 * NT + c] = make_float2(ref[n][e], l[n][e]);
+              float2* dst = reinterpret_cast<float2*>(o + c * D + g * (D / 8));
+#pragma unroll
+              for (int m = 0; m < D / 16; ++m) dst[m] = make_float2(acc[n][m][e], acc[n][m][e + 2]);
+            }
+        }
+      }
+      if (i == n_units) break;
+      // ---- enter the next item: q as B operands, in fp16 at a power of two per row
+      item = next_item;
+      u = u_first = __shfl_sync(0xffffffffu, cur.u, i & 31);
+      b = item / p.items_per_b;
+      const int it = item - b * p.items_per_b;
+      h = it / p.RT;
+      row0 = (it - h * p.RT) * 8 * NT;
+      len = clamp_len(p, b);
+      scores = p.scores ? p.scores + static_cast<long long>(item) * p.cap * (8 * NT) : nullptr;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int r = row0 + 8 * n + g;
+        uint4 w[D / 32];
+        uint32_t mx = 0;
+        const uint16_t* q = nullptr;
+        if (r < p.rows) {
+          const int qi = r / p.G;
+          q = static_cast<const uint16_t*>(a.q) +
+              ((static_cast<long long>(b) * a.nq + qi) * a.Hq + h * p.G + (r - qi * p.G)) * D +
+              (D / 4) * t;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          w[j] = q ? __ldg(reinterpret_cast<const uint4*>(q + 8 * j)) : make_uint4(0, 0, 0, 0);
+          mx = __vmaxu2(mx, __vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu));
+          mx = __vmaxu2(mx, __vmaxu2(w[j].z & 0x7FFF7FFFu, w[j].w & 0x7FFF7FFFu));
+        }
+        mx = max(mx & 0xFFFFu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int eb = static_cast<int>(mx >> 7);  // biased exponent of the row's largest
+        const int up = eb == 0 || eb == 255 ? 0 : min(141 - eb, 127);
+        const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+        const float row_sc = ldexpf(s_unit, -up);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint32_t ww[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            qf[n][2 * j + (e >> 1)][e & 1] = pack_half(__uint_as_float(ww[e] << 16) * f,
+                                                       __uint_as_float(ww[e] & 0xFFFF0000u) * f);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[n][e] = __shfl_sync(0xffffffffu, row_sc, 4 * (2 * t + e));
+          const int rr = row0 + 8 * n + 2 * t + e;
+          lim[n][e] = rr < p.rows ? len - a.nq + rr / p.G : -1;  // last key of the row
+          ref[n][e] = kLowest;
+          l[n][e] = 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[n][m][e] = 0.f;
+      }
+    }
+    // ---- one unit
+    __syncwarp();  // every lane has read unit i - 1, whose stage the next load fills
+    issue(i + S - 1, i >> 5);
+    const float kr = __shfl_sync(0xffffffffu, cur.kr, i & 31);
+    const float vr = __shfl_sync(0xffffffffu, cur.vr, i & 31);
+    const bool there = __shfl_sync(0xffffffffu, cur.row, i & 31) >= 0;
+    ok = __all_sync(0xffffffffu, wait_bar(&bars[i % S], (i / S) & 1, abort_flag, kSiteKv8));
+    if (!ok) break;
+    const int tok0 = u * kUnit;
+    ++u;
+    const uint8_t* stage = ring + (i % S) * 2 * C::kHalf;
+    float s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      const uint4 ka = *reinterpret_cast<const uint4*>(stage + (k_off[0] ^ (j << 4)));
+      const uint4 kb = *reinterpret_cast<const uint4*>(stage + (k_off[1] ^ (j << 4)));
+      const uint32_t k0[4] = {ka.x, ka.y, ka.z, ka.w}, k1[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a0, a1, a2, a3;
+        widen<FMT>(k0[w], a0, a2);
+        widen<FMT>(k1[w], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma16816(s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], s[n]);
+      }
+    }
+    uint32_t v[4][D / 32];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (D == 128) {
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + v_off[x]);
+        v[x][0] = w.x; v[x][1] = w.y; v[x][2 % (D / 32)] = w.z; v[x][3 % (D / 32)] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(stage + v_off[x]);
+        v[x][0] = w.x; v[x][1] = w.y;
+      }
+    }
+    // keys up to len - nq are seen by every row
+    const bool edge = tok0 + kUnit - 1 > len - a.nq || !there || p.rows - row0 < 8 * NT;
+    uint32_t pb[NT][2];
+    float vf[NT][2];
+    if (edge) {  // bytes behind the last token may hold anything, NaN codes among it
+      const int left = there ? len - tok0 : 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (2 * t + (x & 1) + 8 * (x >> 1) >= left)
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) v[x][w] = 0;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float f0 = sc[n][0] * kr, f1 = sc[n][1] * kr;
+      s[n][0] *= f0; s[n][1] *= f1; s[n][2] *= f0; s[n][3] *= f1;
+      vf[n][0] = vf[n][1] = vr * (1.f / full<FMT>());
+      if (edge) {
+        // tokens of the unit that each of the thread's rows sees
+        const int see0 = there ? lim[n][0] - tok0 + 1 : 0, see1 = there ? lim[n][1] - tok0 + 1 : 0;
+        if (g >= see0) s[n][0] = -INFINITY;
+        if (g >= see1) s[n][1] = -INFINITY;
+        if (g + 8 >= see0) s[n][2] = -INFINITY;
+        if (g + 8 >= see1) s[n][3] = -INFINITY;
+        // a row that sees nothing of the unit takes nothing from it, not even a NaN range
+        if (see0 <= 0) vf[n][0] = 0.f;
+        if (see1 <= 0) vf[n][1] = 0.f;
+      }
+      if (scores) {
+        float* at = scores + (static_cast<long long>(tok0) + g) * (8 * NT) + 8 * n + 2 * t;
+        if (tok0 + g < len) *reinterpret_cast<float2*>(at) = make_float2(s[n][0], s[n][1]);
+        if (tok0 + g + 8 < len)
+          *reinterpret_cast<float2*>(at + 64 * NT) = make_float2(s[n][2], s[n][3]);
+      }
+      const float over = fmaxf(fmaxf(s[n][0], s[n][2]) - ref[n][0],
+                               fmaxf(s[n][1], s[n][3]) - ref[n][1]);
+      if (__any_sync(0xffffffffu, over > kSlack)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = fmaxf(s[n][e], s[n][e + 2]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          m = fmaxf(m, ref[n][e]);
+          const float f = ex2(ref[n][e] - m);
+          ref[n][e] = m;
+          l[n][e] *= f;
+#pragma unroll
+          for (int m2 = 0; m2 < D / 16; ++m2) {
+            acc[n][m2][e] *= f;
+            acc[n][m2][e + 2] *= f;
+          }
+        }
+      }
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = ex2(s[n][e] - (ref[n][e & 1] - kLift));
+      l[n][0] += pr[0] + pr[2];
+      l[n][1] += pr[1] + pr[3];
+      pb[n][0] = transpose8x8(pack_half(pr[0], pr[1]));
+      pb[n][1] = transpose8x8(pack_half(pr[2], pr[3]));
+    }
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t x01 = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
+        const uint32_t x23 = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
+        uint32_t a0, a1, a2, a3;
+        widen<FMT>(x01, a0, a1);
+        widen<FMT>(x23, a2, a3);
+        const int m = 2 * w + half;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float d[4];
+          mma16816(d, a0, a1, a2, a3, pb[n][0], pb[n][1], zero);
+          acc[n][m][0] = fmaf(d[0], vf[n][0], acc[n][m][0]);
+          acc[n][m][1] = fmaf(d[1], vf[n][1], acc[n][m][1]);
+          acc[n][m][2] = fmaf(d[2], vf[n][0], acc[n][m][2]);
+          acc[n][m][3] = fmaf(d[3], vf[n][1], acc[n][m][3]);
+        }
+      }
+    }
+  }
+  if (!ok) {  // gave up on a load: let those in flight land before the memory goes away
+    for (int i = 0; i < S; ++i) drain_wait(&bars[i], 0), drain_wait(&bars[i], 1);
+  }
+  __syncthreads();
+  if (*abort_flag) return;
+
+  // Join the warps' partials of each item, in order.
+  for (int s0 = 0; s0 < 2 * kAttnWarps;) {
+    const int item = s_item[s0];
+    if (item < 0) {
+      ++s0;
+      continue;
+    }
+    int s1 = s0 + 1;
+    while (s1 < 2 * kAttnWarps && (s_item[s1] < 0 || s_item[s1] == item)) ++s1;
+    const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
+    const int U = (pre[ib + 1] - pre[ib]) / p.items_per_b, h = it / p.RT, rt = it - h * p.RT;
+    const int U0 = pre[ib] + it * U;
+    const bool whole = cs <= U0 && U0 + U <= ce;
+    const int slot = 2 * cta + (U0 > cs);
+    for (int i = tid; i < 8 * NT * (D / 4); i += kAttnThreads) {
+      const int c = i / (D / 4), d4 = i - c * (D / 4);
+      float m = kLowest;
+      for (int s = s0; s < s1; ++s)
+        if (s_item[s] == item) m = fmaxf(m, s_ml[s * 8 * NT + c].x);
+      float ls = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = s0; s < s1; ++s) {
+        if (s_item[s] != item) continue;
+        const float2 ml = s_ml[s * 8 * NT + c];
+        const float f = ex2(ml.x - m);
+        const float* src = s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kWarpRing)
+                                 : p.warp_o + (static_cast<long long>(cta) * kAttnWarps + (s >> 1)) *
+                                                  8 * NT * D;
+        const float4 v = *reinterpret_cast<const float4*>(src + c * D + 4 * d4);
+        ls += ml.y * f;
+        o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+      }
+      if (whole) {
+        const int rr = rt * 8 * NT + c;
+        const bool some = ls != 0.f;
+        if (p.lse && d4 == 0)
+          p.lse[static_cast<long long>(item) * (8 * NT) + c] =
+              some ? m - kLift + log2f(ls) : INFINITY;
+        if (rr < p.rows) {
+          const float inv = some ? 1.f / ls : 0.f;
+          uint16_t* dst = out_row<D>(p, ib, h, rr) + 4 * d4;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(sm100::pack_bf16x2(o.x * inv, o.y * inv),
+                                                      sm100::pack_bf16x2(o.z * inv, o.w * inv));
+        }
+      } else {
+        reinterpret_cast<float4*>(p.part_o)[(static_cast<long long>(slot) * 8 * NT + c) * (D / 4) + d4] = o;
+        if (d4 == 0) p.part_ml[static_cast<long long>(slot) * 8 * NT + c] = make_float2(m, ls);
+      }
+    }
+    s0 = s1;
+  }
+}
+
+// One CTA per (item, row): joins the partials of an item that was cut between
+// CTAs, in their order; writes the zeros of a sequence without tokens.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
+  constexpr int V = D / 4, GR = 128 / V;  // float4 lanes of a row, groups of partials
+  const int item = blockIdx.x, c = blockIdx.y, t = threadIdx.x;
+  const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
+  const int h = it / p.RT, rt = it - h * p.RT, rr = rt * 8 * NT + c;
+  long long before = 0, T = 0;
+  for (int b = t; b < p.a.B; b += 128) {
+    const long long x = (clamp_len(p, b) + kUnit - 1) / kUnit;
+    T += x;
+    if (b < ib) before += x;
+  }
+  __shared__ long long s_sum[2][4];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    T += __shfl_xor_sync(0xffffffffu, T, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if ((t & 31) == 0) { s_sum[0][t >> 5] = T; s_sum[1][t >> 5] = before; }
+  __syncthreads();
+  T = (s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * p.items_per_b;
+  const int U = (clamp_len(p, ib) + kUnit - 1) / kUnit;
+  const long long U0 = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * p.items_per_b +
+                       static_cast<long long>(it) * U;
+  const int lane4 = t % V, grp = t / V;
+  if (U == 0) {
+    if (rr < p.rows && grp == 0)
+      *reinterpret_cast<uint2*>(out_row<D>(p, ib, h, rr) + 4 * lane4) = make_uint2(0, 0);
+    return;
+  }
+  const int parts = parts_of(T, p.grid);
+  // part of unit x: the last c with floor(c T / parts) <= x
+  const int c0 = static_cast<int>(((U0 + 1) * parts - 1) / T);
+  const int c1 = static_cast<int>(((U0 + U) * parts - 1) / T);
+  if (c0 == c1) return;
+  const int first = 2 * c0 + (T * c0 / parts < U0);
+  __shared__ float4 s_o[GR][V];
+  __shared__ float2 s_ml[GR];
+  float m = kLowest;
+  for (int k = c0 + grp; k <= c1; k += GR)
+    m = fmaxf(m, p.part_ml[static_cast<long long>(k == c0 ? first : 2 * k) * 8 * NT + c].x);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int k = c0 + grp; k <= c1; k += GR) {
+    const long long at = static_cast<long long>(k == c0 ? first : 2 * k) * 8 * NT + c;
+    const float2 ml = p.part_ml[at];
+    const float4 v = reinterpret_cast<const float4*>(p.part_o)[at * V + lane4];
+    const float f = ex2(ml.x - m);
+    l += ml.y * f;
+    o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+  }
+  s_o[grp][lane4] = o;
+  if (lane4 == 0) s_ml[grp] = make_float2(m, l);
+  __syncthreads();
+  if (grp != 0) return;
+  m = kLowest;
+#pragma unroll
+  for (int k = 0; k < GR; ++k) m = fmaxf(m, s_ml[k].x);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < GR; ++k) {
+    const float f = ex2(s_ml[k].x - m);
+    const float4 v = s_o[k][lane4];
+    l += s_ml[k].y * f;
+    o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+  }
+  const bool some = l != 0.f;
+  if (p.lse && lane4 == 0)
+    p.lse[static_cast<long long>(item) * (8 * NT) + c] = some ? m - kLift + log2f(l) : INFINITY;
+  if (rr >= p.rows) return;
+  const float inv = some ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(out_row<D>(p, ib, h, rr) + 4 * lane4) =
+      make_uint2(sm100::pack_bf16x2(o.x * inv, o.y * inv), sm100::pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+// The weight of each key: sum over the kv head's rows of 2^(s - lse).
+template <int NT>
+__global__ void __launch_bounds__(256) weight_kernel(const AttnP p) {
+  const int bh = blockIdx.y, b = bh / p.a.c.Hkv, h = bh - b * p.a.c.Hkv;
+  const long long len = min(static_cast<long long>(clamp_len(p, b)), p.a.weights_stride);
+  for (long long j = blockIdx.x * 256LL + threadIdx.x; j < len; j += gridDim.x * 256LL) {
+    float w = 0.f;
+    for (int rt = 0; rt < p.RT; ++rt) {
+      const long long item = static_cast<long long>(b) * p.items_per_b + h * p.RT + rt;
+      const float4* s = reinterpret_cast<const float4*>(p.scores + (item * p.cap + j) * (8 * NT));
+      const float4* z = reinterpret_cast<const float4*>(p.lse + item * (8 * NT));
+#pragma unroll
+      for (int n = 0; n < 2 * NT; ++n) {
+        const float4 x = s[n], y = z[n];
+        w += (ex2(x.x - y.x) + ex2(x.y - y.y)) + (ex2(x.z - y.z) + ex2(x.w - y.w));
+      }
+    }
+    float* dst = p.a.weights + static_cast<long long>(bh) * p.a.weights_stride + j;
+    *dst = p.a.accumulate ? *dst + w : w;
+  }
+}
+
+struct AttnLayout {
+  int NT, RT;
+  long long part_o, part_ml, warp_o, lse, scores, total;
+};
+
+AttnLayout attn_layout(int B, int nq, int Hq, int Hkv, int D, int max_pages, int page,
+                       int with_weights) {
+  auto al = [](long long x) { return (x + 255) / 256 * 256; };
+  AttnLayout l;
+  const int rows = nq * (Hq / Hkv);
+  l.NT = rows > 8 ? 2 : 1;
+  l.RT = (rows + 8 * l.NT - 1) / (8 * l.NT);
+  const long long slots = 2LL * kMaxSms * (l.NT == 1 ? 2 : 1) * 8 * l.NT;
+  const long long items = static_cast<long long>(B) * Hkv * l.RT;
+  l.part_o = 0;
+  l.part_ml = al(slots * D * 4);
+  l.warp_o = l.part_ml + al(slots * 8);
+  l.lse = l.warp_o + al(slots / 2 * kAttnWarps * D * 4);
+  l.scores = l.lse + (with_weights ? al(items * 8 * l.NT * 4) : 0);
+  l.total = l.scores + (with_weights ? al(items * 8 * l.NT * max_pages * page * 4) : 0);
+  return l;
+}
+
+// The codes of a pool as rows of 128 bytes, one unit a box, 128-byte swizzle.
+template <int D>
+int encode_codes(CUtensorMap* m, const void* codes, const Kv8Cache& c) {
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(c.num_pages) * c.Hkv * c.page * D / 128};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, kUnit * D / 128};
+  const cuuint32_t estr[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? TM_OK
+             : TM_ERR_CUDA;
+}
+
+template <int D, int FMT, int NT>
+int attn_run(AttnP& p, DeviceInfo* di) {
+  using C = AttnCfg<D, NT>;
+  const Kv8AttnArgs& a = p.a;
+  constexpr int kidx = (D == 128) * 4 + (FMT == TM_KV_E4M3) * 2 + (NT == 2);
+  if (int rc = set_smem_once(di->kv8_attr_set[kidx], attn_kernel8<D, FMT, NT>,
+                             C::kSmem + 4 * kMaxAttnBatch))
+    return rc;
+  CUtensorMap tk, tv;
+  if (encode_codes<D>(&tk, a.c.k8, a.c) || encode_codes<D>(&tv, a.c.v8, a.c)) return TM_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+  p.grid = std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1);
+  attn_kernel8<D, FMT, NT><<<p.grid, kAttnThreads, C::kSmem + a.B * 4, st>>>(tk, tv, p);
+  const dim3 grid(static_cast<unsigned>(a.B * p.items_per_b), 8 * NT);
+  combine_kernel<D, NT><<<grid, 128, 0, st>>>(p);
+  if (!p.scores) return counted(2);
+  const long long want = (p.cap + 1023) / 1024;
+  weight_kernel<NT><<<dim3(static_cast<unsigned>(want < 256 ? want : 256), a.B * a.c.Hkv), 256, 0,
+                      st>>>(p);
+  return counted(3);
+}
+
+template <int D, int FMT>
+int attn_nt(AttnP& p, int NT, DeviceInfo* di) {
+  return NT == 1 ? attn_run<D, FMT, 1>(p, di) : attn_run<D, FMT, 2>(p, di);
+}
+
+}  // namespace
+
+long long kv8_attn_workspace_bytes(int B, int nq, int Hq, int Hkv, int D, int max_pages, int page,
+                                   int with_weights) {
+  return attn_layout(B, nq, Hq, Hkv, D, max_pages, page, with_weights).total;
+}
+
+int launch_kv8_attn(const Kv8AttnArgs& a) {
+  DeviceInfo* di = nullptr;
+  if (int rc = device_info(&di)) return rc;
+  const AttnLayout l = attn_layout(a.B, a.nq, a.Hq, a.c.Hkv, a.c.D, a.max_pages, a.c.page,
+                                   a.weights != nullptr);
+  if (a.ws_bytes < l.total) return TM_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  AttnP p;
+  p.a = a;
+  p.G = a.Hq / a.c.Hkv;
+  p.rows = a.nq * p.G;
+  p.RT = l.RT;
+  p.items_per_b = a.c.Hkv * l.RT;
+  p.page_log = a.c.page == 16 ? 4 : a.c.page == 32 ? 5 : a.c.page == 64 ? 6 : 7;
+  p.cap = static_cast<long long>(a.max_pages) * a.c.page;
+  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+  p.warp_o = reinterpret_cast<float*>(ws + l.warp_o);
+  p.lse = a.weights ? reinterpret_cast<float*>(ws + l.lse) : nullptr;
+  p.scores = a.weights ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
+  if (a.c.D == 128)
+    return a.c.format == TM_KV_INT8 ? attn_nt<128, TM_KV_INT8>(p, l.NT, di)
+                                    : attn_nt<128, TM_KV_E4M3>(p, l.NT, di);
+  return a.c.format == TM_KV_INT8 ? attn_nt<64, TM_KV_INT8>(p, l.NT, di)
+                                  : attn_nt<64, TM_KV_E4M3>(p, l.NT, di);
+}
