@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   const Kv8AttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar) + warp * S;
+  asm volatile("griddepcontrol.launch_dependents;");  // the join may take its place early
   if (tid < 2 * kAttnWarps) s_item[tid] = -1;
   if (tid == 0) {
     *abort_flag = 0;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
 // One CTA per (item, row): joins the partials of an item that was cut between
 // CTAs, in their order; writes the zeros of a sequence without tokens.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
+__global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
   constexpr int V = D / 4, GR = 128 / V;  // float4 lanes of a row, groups of partials
   const int item = blockIdx.x, c = blockIdx.y, t = threadIdx.x;
   const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
@@ -605,6 +606,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
   const long long U0 = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * p.items_per_b +
                        static_cast<long long>(it) * U;
   const int lane4 = t % V, grp = t / V;
+  // What is above reads only lens. The rest reads what the kernel before wrote, or
+  // may be read by work that follows this launch.
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (U == 0) {
     if (rr < p.rows && grp == 0)
       *reinterpret_cast<uint2*>(out_row<D>(p, ib, h, rr) + 4 * lane4) = make_uint2(0, 0);
@@ -658,9 +663,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
 
 // The weight of each key: sum over the kv head's rows of 2^(s - lse).
 template <int NT>
-__global__ void __launch_bounds__(256) weight_kernel(const AttnP p) {
+__global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
   const int bh = blockIdx.y, b = bh / p.a.c.Hkv, h = bh - b * p.a.c.Hkv;
   const long long len = min(static_cast<long long>(clamp_len(p, b)), p.a.weights_stride);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (long long j = blockIdx.x * 256LL + threadIdx.x; j < len; j += gridDim.x * 256LL) {
     float w = 0.f;
     for (int rt = 0; rt < p.RT; ++rt) {
@@ -716,6 +722,24 @@ int encode_codes(CUtensorMap* m, const void* codes, const Kv8Cache& c) {
              : TM_ERR_CUDA;
 }
 
+// A launch that may begin before the kernel ahead of it on the stream has ended
+// (it waits for it with griddepcontrol.wait).
+template <class P>
+int launch_early(void (*kernel)(P), dim3 grid, int threads, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return TM_OK;
+  cudaGetLastError();
+  return TM_ERR_CUDA;
+}
+
 template <int D, int FMT, int NT>
 int attn_run(AttnP& p, DeviceInfo* di) {
   using C = AttnCfg<D, NT>;
@@ -730,11 +754,11 @@ int attn_run(AttnP& p, DeviceInfo* di) {
   p.grid = std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1);
   attn_kernel8<D, FMT, NT><<<p.grid, kAttnThreads, C::kSmem + a.B * 4, st>>>(tk, tv, p);
   const dim3 grid(static_cast<unsigned>(a.B * p.items_per_b), 8 * NT);
-  combine_kernel<D, NT><<<grid, 128, 0, st>>>(p);
+  if (launch_early(combine_kernel<D, NT>, grid, 128, st, p)) return TM_ERR_CUDA;
   if (!p.scores) return counted(2);
   const long long want = (p.cap + 1023) / 1024;
-  weight_kernel<NT><<<dim3(static_cast<unsigned>(want < 256 ? want : 256), a.B * a.c.Hkv), 256, 0,
-                      st>>>(p);
+  const dim3 wgrid(static_cast<unsigned>(want < 256 ? want : 256), a.B * a.c.Hkv);
+  if (launch_early(weight_kernel<NT>, wgrid, 256, st, p)) return TM_ERR_CUDA;
   return counted(3);
 }
 
