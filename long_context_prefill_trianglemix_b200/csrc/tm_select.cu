@@ -4,10 +4,16 @@
 //
 // A radix selection: weights map to 32-bit keys that order as they do, and three
 // passes over the row (11, 11 and 10 bits) find the smallest kept key T by
-// histograms from the top; a fourth writes the tokens above T and the first of
-// those equal to it. One thread-block cluster per row shares the histograms
-// through distributed shared memory, so a long row uses several SMs and the
-// whole selection is one launch.
+// histograms from the top; then the tokens above T and the first of those equal
+// to it are written in order. One thread-block cluster per row shares the
+// histograms through distributed shared memory, so a long row uses several SMs
+// and the whole selection is one launch.
+//
+// Latency bounds it (a row of 131072 weights is 0.5 MB): each warp owns a
+// contiguous run and keeps its keys in registers, 16 a lane, so that a part of
+// up to 16384 weights is read once, its loads all in flight together; ranks
+// come from ballots and one scan over the warps; each pass has its own
+// histogram, so a pass costs one cluster barrier.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -24,20 +30,19 @@ namespace cg = cooperative_groups;
 constexpr int kSelThreads = 1024;
 constexpr int kSelMaxCluster = 8;
 constexpr int kBins = 2048;
+constexpr int kSelMaxKeys = 16;  // keys a lane holds at most
 
-struct SelParams {
-  KvSelectArgs a;
-  int cached;  // keys of a CTA's part that fit its shared memory
-};
-
+// 1 for NaN, 0x007FFFFF (-inf) to 0xFF800000 (+inf) otherwise; 0 is left for no weight
+// and 0xFFFFFFFF for a protected one.
 __device__ __forceinline__ uint32_t sort_key(float w) {
-  if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 counts as 0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+  return w == w ? k : 1u;
 }
 
-// Exclusive prefix of v over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+// Exclusive prefix of v over the CTA's threads (each warp's last lane keeps its
+// warp's sum in part[]); the caller synchronises before part is used again.
+__device__ __forceinline__ int block_scan(int v, int* part) {
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   int x = v;
 #pragma unroll
@@ -47,32 +52,28 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   }
   if (lane == 31) part[w] = x;
   __syncthreads();
-  if (w == 0) {
-    int s = part[lane];
+  int before = lane < w ? part[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    part[lane] = s;
-  }
-  __syncthreads();
-  const int before = w ? part[w - 1] : 0;
-  *total = part[31];
-  __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelParams p) {
-  const KvSelectArgs& a = p.a;
-  extern __shared__ uint32_t s_keys[];
-  __shared__ int hist[kBins];
-  __shared__ int part[32];
-  __shared__ int s_pick[2];   // chosen bin, kept tokens above it
-  __shared__ int s_count[2];  // this CTA's tokens above T, equal to T
+// KPL: keys a lane holds (of a round; a part of more than 1024 KPL weights takes
+// several rounds and reads them again in every pass).
+template <int KPL>
+__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectArgs a) {
+  constexpr int kRun = 32 * KPL;  // weights of a warp in a round
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ int part[2][32];
+  __shared__ int s_pick[2];           // chosen bin, kept tokens above it
+  __shared__ int s_gt[32], s_eq[32];  // per warp: tokens above T, equal to T
+  __shared__ int s_count[2];          // the same of this CTA
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  const int row = blockIdx.x / C, b = row / a.H, t = threadIdx.x;
+  const int row = blockIdx.x / C, b = row / a.H, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  for (int i = t; i < 3 * kBins / 4; i += kSelThreads)
+    reinterpret_cast<int4*>(&hist[0][0])[i] = make_int4(0, 0, 0, 0);
+  if (t < 2) s_count[t] = 0;
   const int n = min(max(a.lens ? a.lens[b] : a.n, 0), a.n);
   int* out = a.index + static_cast<long long>(row) * a.keep;
   const int kept = min(n, a.keep);
@@ -85,41 +86,76 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelParams 
   const float* w = a.weights + static_cast<long long>(row) * a.stride;
   const int per = (n + C - 1) / C;
   const int lo = min(rank * per, n), hi = min(lo + per, n);
-  const int cached = min(hi - lo, p.cached);
-  auto fresh = [&](int i) {
-    return i < a.sinks || i >= n - a.recent ? 0xFFFFFFFFu : sort_key(w[i]);
-  };
-  auto key_of = [&](int i) { return i - lo < cached ? s_keys[i - lo] : fresh(i); };
+  const int rounds = (hi - lo + kSelThreads * KPL - 1) / (kSelThreads * KPL);
 
-  uint32_t prefix = 0, mask = 0;
-  int need = kept;  // tokens still to take among those that match the prefix
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t bins = pass == 2 ? 1024u : 2048u;
-    for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = lo + t; i < hi; i += kSelThreads) {
-      uint32_t key;
-      if (pass == 0) {
-        key = fresh(i);
-        if (i - lo < cached) s_keys[i - lo] = key;
-      } else {
-        key = key_of(i);
-      }
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+  // Round r: warp v holds weights base + k 32 + lane, k < KPL, of its run.
+  uint32_t key[KPL];
+  int base = 0;
+  bool any = false;  // the warp's run holds a weight
+  auto load = [&](int r) {
+    base = lo + r * kSelThreads * KPL + warp * kRun;
+    any = base < hi;
+    if (!any) return;
+    const float* at = w + base + lane;
+    if (base + kRun <= hi) {
+      float x[KPL];
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) x[k] = __ldg(at + 32 * k);
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) key[k] = sort_key(x[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < KPL; ++k)
+        key[k] = base + 32 * k + lane < hi ? sort_key(__ldg(at + 32 * k)) : 0u;
     }
-    cluster.sync();
+    if (base < a.sinks || base + kRun > n - a.recent) {
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) {
+        const int i = base + 32 * k + lane;
+        if (i < hi && (i < a.sinks || i >= n - a.recent)) key[k] = 0xFFFFFFFFu;
+      }
+    }
+  };
+  load(0);
+  __syncthreads();
+
+  uint32_t prefix = 0;
+  int need = kept;  // tokens still to take among those that match the prefix
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    constexpr int kShift[3] = {21, 10, 0};
+    const int shift = kShift[pass];
+    const uint32_t bins = pass == 2 ? 1024u : 2048u;
+    for (int r = 0; r < rounds; ++r) {
+      if (rounds > 1) load(r);
+      if (!any) continue;
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) {
+        if (pass == 0)
+          atomicAdd(&hist[0][key[k] >> 21], 1);
+        else if ((key[k] ^ prefix) >> kShift[pass > 0 ? pass - 1 : 0] == 0)
+          atomicAdd(&hist[pass][(key[k] >> shift) & (bins - 1)], 1);
+      }
+    }
+    if (C > 1) cluster.sync(); else __syncthreads();
     // bins from the top: thread t owns the two bins 2047 - 2t, 2046 - 2t
     const int b1 = kBins - 1 - 2 * t, b0 = b1 - 1;
     int c1 = 0, c0 = 0;
-    for (int r = 0; r < C; ++r) {
-      const int* h = cluster.map_shared_rank(hist, r);
-      c1 += h[b1];
-      c0 += h[b0];
+    if (C == 1) {
+      const int2 h = *reinterpret_cast<const int2*>(&hist[pass][b0]);
+      c0 = h.x;
+      c1 = h.y;
+    } else {
+#pragma unroll
+      for (int r = 0; r < kSelMaxCluster; ++r) {
+        if (r < C) {
+          const int2 h = *reinterpret_cast<const int2*>(cluster.map_shared_rank(&hist[pass][b0], r));
+          c0 += h.x;
+          c1 += h.y;
+        }
+      }
     }
-    int total;
-    const int above = block_scan(c1 + c0, part, &total);
+    const int above = block_scan(c1 + c0, part[pass & 1]);
     if (above < need && above + c1 >= need) {
       s_pick[0] = b1;
       s_pick[1] = above;
@@ -127,43 +163,78 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelParams 
       s_pick[0] = b0;
       s_pick[1] = above + c1;
     }
-    cluster.sync();  // every CTA has read the histograms; s_pick is visible
+    __syncthreads();
     prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
-    mask |= (bins - 1) << shift;
     need -= s_pick[1];
+    __syncthreads();  // s_pick has been read
   }
   // prefix is T; `need` tokens equal to it are kept, the first ones of the row.
-  if (t < 2) s_count[t] = 0;
-  __syncthreads();
+  auto count = [&](int& gt, int& eq) {
+    gt = eq = 0;
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) {
+        gt += key[k] > prefix;
+        eq += key[k] == prefix;
+      }
+      gt = __reduce_add_sync(0xffffffffu, gt);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+    }
+  };
   int gt = 0, eq = 0;
-  for (int i = lo + t; i < hi; i += kSelThreads) {
-    const uint32_t key = key_of(i);
-    gt += key > prefix;
-    eq += key == prefix;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) load(r);
+    int g, e;
+    count(g, e);
+    gt += g;
+    eq += e;
   }
-  atomicAdd(&s_count[0], gt);
-  atomicAdd(&s_count[1], eq);
-  cluster.sync();
+  if (lane == 0) {
+    s_gt[warp] = gt;
+    s_eq[warp] = eq;
+    atomicAdd(&s_count[0], gt);
+    atomicAdd(&s_count[1], eq);
+  }
+  if (C > 1) cluster.sync(); else __syncthreads();
   int gt_before = 0, eq_before = 0;
   for (int r = 0; r < rank; ++r) {
     const int* c = cluster.map_shared_rank(s_count, r);
     gt_before += c[0];
     eq_before += c[1];
   }
-  int pos = gt_before + min(eq_before, need);
-  for (int i0 = lo; i0 < hi; i0 += kSelThreads) {
-    const int i = i0 + t;
-    const uint32_t key = i < hi ? key_of(i) : 0u;
-    const bool is_eq = i < hi && key == prefix;
-    int n_eq, n_keep;
-    const int eq_at = block_scan(is_eq, part, &n_eq);
-    const bool take = i < hi && (key > prefix || (is_eq && eq_before + eq_at < need));
-    const int at = block_scan(take, part, &n_keep);
-    if (take) out[pos + at] = i;
-    pos += n_keep;
-    eq_before += n_eq;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) {  // this round's counts of each warp
+      load(r);
+      int g, e;
+      count(g, e);
+      __syncthreads();
+      if (lane == 0) {
+        s_gt[warp] = g;
+        s_eq[warp] = e;
+      }
+      __syncthreads();
+    }
+    const int wg = s_gt[lane], we = s_eq[lane];
+    if (any) {
+      int g0 = gt_before + __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0);
+      int e0 = eq_before + __reduce_add_sync(0xffffffffu, lane < warp ? we : 0);
+      const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) {
+        const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > prefix);
+        const uint32_t be = __ballot_sync(0xffffffffu, key[k] == prefix);
+        if ((bg | be) == 0) continue;
+        const int eq_at = e0 + __popc(be & below);
+        if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && eq_at < need))
+          out[g0 + __popc(bg & below) + min(eq_at, need)] = base + 32 * k + lane;
+        g0 += __popc(bg);
+        e0 += __popc(be);
+      }
+    }
+    gt_before += __reduce_add_sync(0xffffffffu, wg);
+    eq_before += __reduce_add_sync(0xffffffffu, we);
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 }  // namespace
@@ -176,18 +247,9 @@ int launch_kv_select(const KvSelectArgs& a) {
   int C = 1;
   const long long rows = static_cast<long long>(a.B) * a.H;
   while (C < kSelMaxCluster && a.n > 4096LL * C && rows * C * 2 <= sms) C *= 2;
-  const int per = (a.n + C - 1) / C;
-  SelParams p;
-  p.a = a;
-  p.cached = per < 40960 ? per : 40960;
-  const int smem = p.cached * 4;
-  if (cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 40960 * 4) !=
-      cudaSuccess)
-    return TM_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(a.stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -196,7 +258,12 @@ int launch_kv_select(const KvSelectArgs& a) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, select_kernel, p) != cudaSuccess) {
+  const int per = (a.n + C - 1) / C;
+  auto kernel = per <= 2 * kSelThreads   ? select_kernel<2>
+                : per <= 4 * kSelThreads ? select_kernel<4>
+                : per <= 8 * kSelThreads ? select_kernel<8>
+                                         : select_kernel<kSelMaxKeys>;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
     cudaGetLastError();
     return TM_ERR_CUDA;
   }
