@@ -40,22 +40,14 @@ __device__ __forceinline__ uint32_t sort_key(float w) {
   return w == w ? k : 1u;
 }
 
-// Exclusive prefix of v over the CTA's threads (each warp's last lane keeps its
-// warp's sum in part[]); the caller synchronises before part is used again.
-__device__ __forceinline__ int block_scan(int v, int* part) {
-  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-  int x = v;
+// The sum of v over the lanes above this one, and its own included.
+__device__ __forceinline__ int sum_from_above(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_down_sync(0xffffffffu, v, o);
+    if (lane + o < 32) v += y;
   }
-  if (lane == 31) part[w] = x;
-  __syncthreads();
-  int before = lane < w ? part[lane] : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  return before + x - v;
+  return v;
 }
 
 // KPL: keys a lane holds (of a round; a part of more than 1024 KPL weights takes
@@ -64,7 +56,7 @@ template <int KPL>
 __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectArgs a) {
   constexpr int kRun = 32 * KPL;  // weights of a warp in a round
   __shared__ __align__(16) int hist[3][kBins];
-  __shared__ int part[2][32];
+  __shared__ int coarse[3][32];       // sums of 64 bins
   __shared__ int s_pick[2];           // chosen bin, kept tokens above it
   __shared__ int s_gt[32], s_eq[32];  // per warp: tokens above T, equal to T
   __shared__ int s_count[2];          // the same of this CTA
@@ -137,31 +129,40 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectAr
           atomicAdd(&hist[pass][(key[k] >> shift) & (bins - 1)], 1);
       }
     }
+    __syncthreads();
+    {
+      const int2 h = *reinterpret_cast<const int2*>(&hist[pass][64 * warp + 2 * lane]);
+      const int sum = __reduce_add_sync(0xffffffffu, h.x + h.y);
+      if (lane == 0) coarse[pass][warp] = sum;
+    }
     if (C > 1) cluster.sync(); else __syncthreads();
-    // bins from the top: thread t owns the two bins 2047 - 2t, 2046 - 2t
-    const int b1 = kBins - 1 - 2 * t, b0 = b1 - 1;
-    int c1 = 0, c0 = 0;
-    if (C == 1) {
-      const int2 h = *reinterpret_cast<const int2*>(&hist[pass][b0]);
-      c0 = h.x;
-      c1 = h.y;
-    } else {
+    // One warp finds the bin: the 64 it lies in by the coarse sums, then itself. It
+    // reads 3 KB of the other CTAs' memory in two steps instead of their histograms.
+    if (warp == 0) {
+      int c = 0;
+#pragma unroll
+      for (int r = 0; r < kSelMaxCluster; ++r)
+        if (r < C) c += *cluster.map_shared_rank(&coarse[pass][lane], r);
+      int upto = sum_from_above(c, lane);
+      const int top = 31 - __clz(__ballot_sync(0xffffffffu, upto >= need));
+      const int above = __shfl_sync(0xffffffffu, upto - c, top);
+      int2 f = make_int2(0, 0);
 #pragma unroll
       for (int r = 0; r < kSelMaxCluster; ++r) {
         if (r < C) {
-          const int2 h = *reinterpret_cast<const int2*>(cluster.map_shared_rank(&hist[pass][b0], r));
-          c0 += h.x;
-          c1 += h.y;
+          const int2 h = *reinterpret_cast<const int2*>(
+              cluster.map_shared_rank(&hist[pass][64 * top + 2 * lane], r));
+          f.x += h.x;
+          f.y += h.y;
         }
       }
-    }
-    const int above = block_scan(c1 + c0, part[pass & 1]);
-    if (above < need && above + c1 >= need) {
-      s_pick[0] = b1;
-      s_pick[1] = above;
-    } else if (above + c1 < need && above + c1 + c0 >= need) {
-      s_pick[0] = b0;
-      s_pick[1] = above + c1;
+      upto = above + sum_from_above(f.x + f.y, lane);
+      const int in = 31 - __clz(__ballot_sync(0xffffffffu, upto >= need));
+      if (lane == in) {
+        const bool hi_bin = upto - f.x >= need;  // bins above, and the lane's upper one
+        s_pick[0] = 64 * top + 2 * lane + hi_bin;
+        s_pick[1] = hi_bin ? upto - f.x - f.y : upto - f.x;
+      }
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
