@@ -51,6 +51,7 @@
 #include "tm.h"
 #include "tm_internal.h"
 #include "tm_kv8.cuh"
+#include "tm_exp2_poly5.h"
 #include "tm_sm100.cuh"
 #include "tm_tiles.cuh"
 
@@ -1688,9 +1689,20 @@ WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
   l.nkt = (N + BN - 1) / BN;
   // Pass 1 cuts the key range until there are about four items an SM, of four
   // key tiles or more. The count is fixed so that a workspace's size is.
-  const long long pairs = static_cast<long long>(B) * Hkv * ((l.nqt + 1) / 2);
-  l.splits = static_cast<int>(
-      std::max(1LL, std::min<long long>((592 + pairs - 1) / pairs, (l.nkt + 3) / 4)));
+  // Among the counts from there to twice that, the one whose last wave on 148 SMs is fullest.
+  const long long groups = static_cast<long long>(B) * Hkv * ((l.nqt + kWtTiles - 1) / kWtTiles);
+  const long long most = std::max(1, (l.nkt + 3) / 4);
+  const long long base = std::max(1LL, std::min<long long>((592 + groups - 1) / groups, most));
+  double best = 0.0;
+  l.splits = static_cast<int>(base);
+  for (long long x = base; base > 1 && x <= std::min(2 * base, most); ++x) {
+    const long long items = groups * x, waves = (items + 147) / 148;
+    const double fill = static_cast<double>(items) / (waves * 148);
+    if (fill > best + 1e-9) {
+      best = fill;
+      l.splits = static_cast<int>(x);
+    }
+  }
   const long long tile_rows = static_cast<long long>(B) * Hkv * l.nqt * 128;
   l.lse = al(tile_rows * l.splits * 8);
   l.total = l.lse + al(tile_rows * 4);
@@ -1712,7 +1724,7 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
   p.sl2 = a.scale * 1.4426950408889634f;
   p.lens = a.lens;
   p.stats = static_cast<float2*>(a.ws);
-  p.lse = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + l.lse);
+  p.nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + l.lse);
   p.weights = a.weights;
   p.stride = a.stride;
   p.accumulate = a.accumulate;
@@ -1730,11 +1742,11 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
     return TM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
   const long long bg = static_cast<long long>(a.B) * a.Hkv;
-  p.items = static_cast<int>(bg * ((l.nqt + 1) / 2) * l.splits);
+  p.items = static_cast<int>(bg * ((l.nqt + kWtTiles - 1) / kWtTiles) * l.splits);
   weights_kernel<D, 1><<<std::min(p.items, di->sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
   const long long rows = bg * l.nqt * 128;
   weights_lse_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, st>>>(p);
-  p.items = static_cast<int>(bg * ((l.nkt + 1) / 2));
+  p.items = static_cast<int>(bg * ((l.nkt + kWtTiles - 1) / kWtTiles));
   weights_kernel<D, 2><<<std::min(p.items, di->sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
   return counted(3);
 }
