@@ -1321,6 +1321,26 @@ int set_smem_once(std::atomic<bool>& flag, K kernel, int bytes) {
   return TM_OK;
 }
 
+// A launch that may begin before the kernel ahead of it on the stream has ended
+// (it waits for it with griddepcontrol.wait before it touches memory).
+template <class... P, class... A>
+int launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st,
+                 const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return TM_OK;
+  cudaGetLastError();
+  return TM_ERR_CUDA;
+}
+
 int get_encode_fn() {
   if (g_encode) return TM_OK;
   void* fn = nullptr;
@@ -1677,9 +1697,17 @@ int launch_discovery_d(const DiscArgs& a, DeviceInfo* di) {
 
 // Key weights: q tiles of tpt tokens of a group's q heads, and the workspace.
 struct WtLayout {
-  int tpt, nqt, nkt, splits;
+  int tpt, nqt, nkt, splits, q_group;
   long long lse, total;
 };
+// A tiles an item takes: four share each B tile and keep an SM's four warpgroups busy;
+// fewer where that would leave SMs without an item (8 key rows of 33 tiles: 46 us of four, 39 of one).
+int weights_group(long long bg, int tiles) {
+  int g = kWtTiles;
+  while (g > 1 && bg * ((tiles + g - 1) / g) < 148) g /= 2;
+  return g;
+}
+
 WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
   auto al = [](long long x) { return (x + 255) / 256 * 256; };
   WtLayout l;
@@ -1690,7 +1718,9 @@ WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
   // Pass 1 cuts the key range until there are about four items an SM, of four
   // key tiles or more. The count is fixed so that a workspace's size is.
   // Among the counts from there to twice that, the one whose last wave on 148 SMs is fullest.
-  const long long groups = static_cast<long long>(B) * Hkv * ((l.nqt + kWtTiles - 1) / kWtTiles);
+  const long long bg = static_cast<long long>(B) * Hkv;
+  l.q_group = std::min(kWtTiles, l.nqt >= 4 ? 4 : l.nqt >= 2 ? 2 : 1);
+  const long long groups = bg * ((l.nqt + l.q_group - 1) / l.q_group);
   const long long most = std::max(1, (l.nkt + 3) / 4);
   const long long base = std::max(1LL, std::min<long long>((592 + groups - 1) / groups, most));
   double best = 0.0;
@@ -1742,12 +1772,18 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
     return TM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
   const long long bg = static_cast<long long>(a.B) * a.Hkv;
-  p.items = static_cast<int>(bg * ((l.nqt + kWtTiles - 1) / kWtTiles) * l.splits);
-  weights_kernel<D, 1><<<std::min(p.items, di->sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
+  const unsigned sms = static_cast<unsigned>(di->sms);
+  p.group = l.q_group;
+  p.items = static_cast<int>(bg * ((l.nqt + p.group - 1) / p.group) * l.splits);
+  weights_kernel<D, 1><<<std::min<unsigned>(p.items, sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
   const long long rows = bg * l.nqt * 128;
-  weights_lse_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, st>>>(p);
-  p.items = static_cast<int>(bg * ((l.nkt + kWtTiles - 1) / kWtTiles));
-  weights_kernel<D, 2><<<std::min(p.items, di->sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
+  if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), 256, 0, st, p))
+    return TM_ERR_CUDA;
+  p.group = weights_group(bg, l.nkt);
+  p.items = static_cast<int>(bg * ((l.nkt + p.group - 1) / p.group));
+  if (launch_early(weights_kernel<D, 2>, dim3(std::min<unsigned>(p.items, sms)), kWtThreads, C::kSmem,
+                   st, tq, tk, p))
+    return TM_ERR_CUDA;
   return counted(3);
 }
 

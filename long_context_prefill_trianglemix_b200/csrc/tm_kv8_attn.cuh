@@ -722,24 +722,6 @@ int encode_codes(CUtensorMap* m, const void* codes, const Kv8Cache& c) {
              : TM_ERR_CUDA;
 }
 
-// A launch that may begin before the kernel ahead of it on the stream has ended
-// (it waits for it with griddepcontrol.wait).
-template <class P>
-int launch_early(void (*kernel)(P), dim3 grid, int threads, cudaStream_t st, const P& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return TM_OK;
-  cudaGetLastError();
-  return TM_ERR_CUDA;
-}
-
 template <int D, int FMT, int NT>
 int attn_run(AttnP& p, DeviceInfo* di) {
   using C = AttnCfg<D, NT>;
@@ -754,11 +736,11 @@ int attn_run(AttnP& p, DeviceInfo* di) {
   p.grid = std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1);
   attn_kernel8<D, FMT, NT><<<p.grid, kAttnThreads, C::kSmem + a.B * 4, st>>>(tk, tv, p);
   const dim3 grid(static_cast<unsigned>(a.B * p.items_per_b), 8 * NT);
-  if (launch_early(combine_kernel<D, NT>, grid, 128, st, p)) return TM_ERR_CUDA;
+  if (launch_early(combine_kernel<D, NT>, grid, 128, 0, st, p)) return TM_ERR_CUDA;
   if (!p.scores) return counted(2);
   const long long want = (p.cap + 1023) / 1024;
   const dim3 wgrid(static_cast<unsigned>(want < 256 ? want : 256), a.B * a.c.Hkv);
-  if (launch_early(weight_kernel<NT>, wgrid, 256, st, p)) return TM_ERR_CUDA;
+  if (launch_early(weight_kernel<NT>, wgrid, 256, 0, st, p)) return TM_ERR_CUDA;
   return counted(3);
 }
 

@@ -37,59 +37,91 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ void fadd2(float& a0, float& a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
+// Packed pairs of fp32 as 64-bit registers, and the arithmetic on them.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 pack2(uint32_t a, uint32_t b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A constant in both halves, opaque to the compiler: it stays in a register pair
+// instead of being moved there again for every use.
+__device__ __forceinline__ F2 both(float c) {
+  F2 r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(c));
+  return r;
+}
+
+struct Quintic {
+  F2 magic, minus_magic, minus_one, c0, c1, c2, c3, c4, c5;
+};
+__device__ __forceinline__ Quintic quintic() {
+  Quintic k;
+  k.magic = both(12582912.0f);  // 1.5 * 2^23
+  k.minus_magic = both(-12582912.0f);
+  k.minus_one = both(-1.0f);
+  k.c0 = both(TM_EXP2_P5_C0); k.c1 = both(TM_EXP2_P5_C1); k.c2 = both(TM_EXP2_P5_C2);
+  k.c3 = both(TM_EXP2_P5_C3); k.c4 = both(TM_EXP2_P5_C4); k.c5 = both(TM_EXP2_P5_C5);
+  return k;
 }
 
 // 2^x of two values on the FMA pipe, good to 2^-22: x = n + f with n = round(x)
 // (through 1.5 * 2^23), the fitted quintic for 2^f in packed FMAs, times 2^n built
 // in the exponent field. x is clamped at -126 (2^-126 instead of less); NaN stays.
-__device__ __forceinline__ void ex2x2_quintic(float& x0, float& x1) {
-  uint32_t ta, tb;
-  float p0, p1;
-  asm("{\n\t.reg .b64 x, m, t, n, f, p, c;\n\t.reg .f32 u, v;\n\t"
-      "max.NaN.f32 u, %4, 0fC2FC0000;\n\t"
-      "max.NaN.f32 v, %5, 0fC2FC0000;\n\t"
-      "mov.b64 x, {u, v};\n\t"
-      "mov.b64 m, {%6, %6};\n\t"
-      "add.rn.f32x2 t, x, m;\n\t"
-      "sub.rn.f32x2 n, t, m;\n\t"
-      "sub.rn.f32x2 f, x, n;\n\t"
-      "mov.b64 c, {%7, %7};\n\t"
-      "mov.b64 p, {%8, %8};\n\t"
-      "fma.rn.f32x2 p, c, f, p;\n\t"
-      "mov.b64 c, {%9, %9};\n\t"
-      "fma.rn.f32x2 p, p, f, c;\n\t"
-      "mov.b64 c, {%10, %10};\n\t"
-      "fma.rn.f32x2 p, p, f, c;\n\t"
-      "mov.b64 c, {%11, %11};\n\t"
-      "fma.rn.f32x2 p, p, f, c;\n\t"
-      "mov.b64 c, {%12, %12};\n\t"
-      "fma.rn.f32x2 p, p, f, c;\n\t"
-      "mov.b64 {%0, %1}, t;\n\t"
-      "mov.b64 {%2, %3}, p;\n\t}"
-      : "=r"(ta), "=r"(tb), "=f"(p0), "=f"(p1)
-      : "f"(x0), "f"(x1), "f"(12582912.0f), "f"(TM_EXP2_P5_C5), "f"(TM_EXP2_P5_C4),
-        "f"(TM_EXP2_P5_C3), "f"(TM_EXP2_P5_C2), "f"(TM_EXP2_P5_C1), "f"(TM_EXP2_P5_C0));
-  const float sa = __uint_as_float(ta * 8388608u + 0x3F800000u);
-  const float sb = __uint_as_float(tb * 8388608u + 0x3F800000u);
-  x0 = p0 * sa;
-  x1 = p1 * sb;
+__device__ __forceinline__ F2 ex2x2_quintic(const Quintic& k, F2 x) {
+  float xa, xb;
+  unpack2(x, xa, xb);
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(xa));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(xb));
+  x = pack2(xa, xb);
+  const F2 t = add2(x, k.magic);
+  const F2 n = add2(t, k.minus_magic);
+  const F2 f = fma2(n, k.minus_one, x);
+  F2 p = fma2(k.c5, f, k.c4);
+  p = fma2(p, f, k.c3);
+  p = fma2(p, f, k.c2);
+  p = fma2(p, f, k.c1);
+  p = fma2(p, f, k.c0);
+  float ta, tb;
+  unpack2(t, ta, tb);
+  return mul2(p, pack2(__float_as_uint(ta) * 8388608u + 0x3F800000u,
+                       __float_as_uint(tb) * 8388608u + 0x3F800000u));
 }
 
 // kWtPoly of every 8 pairs go to the FMA pipe, the others to MUFU.
-constexpr int kWtPoly = 3;
-__device__ __forceinline__ void wt_exp_pair(int e, float& x0, float& x1) {
-  constexpr uint32_t kMask = kWtPoly == 0 ? 0u : kWtPoly == 2 ? 0x22u : kWtPoly == 3 ? 0x4Au : 0xAAu;
-  if ((kMask >> ((e >> 1) & 7)) & 1u) {
-    ex2x2_quintic(x0, x1);
-  } else {
-    x0 = ex2(x0);
-    x1 = ex2(x1);
-  }
+#ifndef WT_POLY
+#define WT_POLY 2
+#endif
+constexpr int kWtPoly = WT_POLY;
+__device__ __forceinline__ F2 wt_exp_pair(const Quintic& k, int e, F2 x) {
+  constexpr uint32_t kMask = kWtPoly == 0 ? 0u : kWtPoly == 1 ? 0x08u : kWtPoly == 2 ? 0x22u : kWtPoly == 3 ? 0x4Au : 0xAAu;
+  if ((kMask >> ((e >> 1) & 7)) & 1u) return ex2x2_quintic(k, x);
+  float a, b;
+  unpack2(x, a, b);
+  return pack2(ex2(a), ex2(b));
 }
 
 struct WtItem {
@@ -105,7 +137,7 @@ struct WtParams {
   int tpt;           // tokens of a q tile
   int nqt, nkt;      // q tiles, key tiles (of the longest sequence)
   int splits;        // pass 1: parts of the key range
-  int items;
+  int items, group;  // A tiles of an item: 1, 2 or 4
   float sl2;
   const int* lens;
   float2* stats;     // pass 1: (m, l) [B Hkv][splits][nqt * 128]
@@ -151,14 +183,14 @@ __device__ __forceinline__ int wt_len(const WtParams& p, int b) {
 // Item i of a pass; false if it has no work (padding of a shorter sequence).
 template <int PASS>
 __device__ __forceinline__ bool wt_item(const WtParams& p, int i, WtItem& it) {
-  const int groups = ((PASS == 1 ? p.nqt : p.nkt) + kWtTiles - 1) / kWtTiles;
+  const int groups = ((PASS == 1 ? p.nqt : p.nkt) + p.group - 1) / p.group;
   int x = i;
   it.split = 0;
   if (PASS == 1) {
     it.split = x % p.splits;
     x /= p.splits;
   }
-  it.a0 = kWtTiles * (x % groups);
+  it.a0 = p.group * (x % groups);
   x /= groups;
   it.g = x % p.Hkv;
   it.b = x / p.Hkv;
@@ -167,16 +199,16 @@ __device__ __forceinline__ bool wt_item(const WtParams& p, int i, WtItem& it) {
   it.r0 = it.len - rows;
   const int nqt = (rows + p.tpt - 1) / p.tpt;
   if (PASS == 1) {
-    it.na = imin(kWtTiles, nqt - it.a0);
+    it.na = imin(p.group, nqt - it.a0);
     if (it.na <= 0) return false;
     // keys up to the group's last row
-    const int last = it.r0 + imin(rows, (it.a0 + kWtTiles) * p.tpt);
+    const int last = it.r0 + imin(rows, (it.a0 + p.group) * p.tpt);
     const int nk = (last + BN - 1) / BN;
     it.t0 = static_cast<int>(static_cast<long long>(nk) * it.split / p.splits);
     it.t1 = static_cast<int>(static_cast<long long>(nk) * (it.split + 1) / p.splits);
     return true;  // an empty part still writes its (neutral) statistics
   }
-  it.na = imin(kWtTiles, (it.len + BN - 1) / BN - it.a0);
+  it.na = imin(p.group, (it.len + BN - 1) / BN - it.a0);
   if (it.na <= 0) return false;
   // q tiles with a row at or after the group's first key
   it.t0 = imax(0, (it.a0 * BN - it.r0) / p.tpt);
@@ -194,9 +226,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   WtBars* bars = reinterpret_cast<WtBars*>(smem + C::kBar);
   volatile int* abort_flag = &bars->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // rows that a q tile's box does not cover stay zero
-  for (int i = tid; i < C::kLse / 16; i += kWtThreads)
-    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  // Rows that a q tile's box does not cover stay zero (the q tiles are the A tiles in
+  // pass 1 and the ring in pass 2).
+  const int q_rows = p.tpt * p.G, q_tiles = PASS == 1 ? kWtTiles : kWtStages;
+  for (int i = tid; i < (128 - q_rows) * 8 * (D / 64) * q_tiles; i += kWtThreads) {
+    const int panel = i / ((128 - q_rows) * 8), x = i - panel * (128 - q_rows) * 8;
+    reinterpret_cast<uint4*>(smem + (PASS == 1 ? 0 : C::kRing) + panel * C::kPanel + q_rows * 128)[x] =
+        make_uint4(0, 0, 0, 0);
+  }
   if (tid == 0) {
     for (int i = 0; i < kWtTiles; ++i) {
       mbar_init(&bars->a_full[i], 1);
@@ -224,9 +261,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // pass 2: the lse kernel's results
   const uint32_t tmem = bars->tmem;
   const uint32_t sA = smem_addr(smem), sB = sA + C::kRing;
-  const int q_bytes = p.tpt * p.G * D * 2;
+  const int q_bytes = q_rows * D * 2;
 
   if (warp == 4 * kWtTiles) {
     if (lane == 0) {
@@ -333,6 +372,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   } else {
     const int wg = warp >> 2, r = tid & 127;
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const Quintic kq = quintic();
+    const F2 sl2 = both(p.sl2);
     uint32_t bc = 0, sc = 0;  // B tiles of the CTA, scores of this warpgroup
     bool ok = true;
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
@@ -372,7 +413,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           c_hi = imin(p.tpt, rows - t * p.tpt) * p.G;
         }
         const bool full = __all_sync(0xffffffffu, !live || (c_lo == 0 && c_hi == 128));
-        const float4* z = reinterpret_cast<const float4*>(smem + C::kLse + ls * 512);
+        const ulonglong2* z = reinterpret_cast<const ulonglong2*>(smem + C::kLse + ls * 512);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t s[2][32];
@@ -386,7 +427,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (lane == 0) mbar_arrive(&bars->s_empty[wg]);
           }
           if (!warp_live) continue;
-          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+          F2 acc0 = 0, acc1 = 0;  // pairs of zeros
+          float a0 = 0.f;
           if (PASS == 1) {
             if (!full) {
               const int c_end = c_hi - 64 * h;
@@ -410,35 +452,26 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const float mn = fmax3_nan(m, mt, mt);
             sum *= ex2(m - mn);
             m = mn;
+            const F2 minus_m = pack2(-m, -m);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                float x[4];
-                ffma2(x[0], x[1], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]), p.sl2, p.sl2,
-                      -m, -m);
-                ffma2(x[2], x[3], __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]), p.sl2,
-                      p.sl2, -m, -m);
-                wt_exp_pair(e, x[0], x[1]);
-                wt_exp_pair(e + 2, x[2], x[3]);
-                fadd2(a0, a1, x[0], x[1]);
-                fadd2(a2, a3, x[2], x[3]);
+                const F2 x = fma2(pack2(s[c][e], s[c][e + 1]), sl2, minus_m);
+                const F2 y = fma2(pack2(s[c][e + 2], s[c][e + 3]), sl2, minus_m);
+                acc0 = add2(acc0, wt_exp_pair(kq, e, x));
+                acc1 = add2(acc1, wt_exp_pair(kq, e + 2, y));
               }
           } else if (full) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 y = z[16 * h + 8 * c + e / 4];
-                float x[4];
-                ffma2(x[0], x[1], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]), p.sl2, p.sl2,
-                      y.x, y.y);
-                ffma2(x[2], x[3], __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]), p.sl2,
-                      p.sl2, y.z, y.w);
-                wt_exp_pair(e, x[0], x[1]);
-                wt_exp_pair(e + 2, x[2], x[3]);
-                fadd2(a0, a1, x[0], x[1]);
-                fadd2(a2, a3, x[2], x[3]);
+                const ulonglong2 nl = z[16 * h + 8 * c + e / 4];
+                const F2 x = fma2(pack2(s[c][e], s[c][e + 1]), sl2, nl.x);
+                const F2 y = fma2(pack2(s[c][e + 2], s[c][e + 3]), sl2, nl.y);
+                acc0 = add2(acc0, wt_exp_pair(kq, e, x));
+                acc1 = add2(acc1, wt_exp_pair(kq, e + 2, y));
               }
           } else {
             const int lo = c_lo - 64 * h, end = c_hi - 64 * h;
@@ -453,7 +486,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               }
             }
           }
-          sum += (a0 + a1) + (a2 + a3);
+          float r0, r1;
+          unpack2(add2(acc0, acc1), r0, r1);
+          sum += r0 + r1 + a0;
         }
         if (PASS == 2) {
           __syncwarp();
@@ -481,6 +516,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
 // Joins pass 1's parts: -(m + log2(l)) of each row, -inf for a row that is not there.
 __global__ void __launch_bounds__(256) weights_lse_kernel(const WtParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long per = static_cast<long long>(p.nqt) * 128, n = per * p.B * p.Hkv;
   const long long i = blockIdx.x * 256LL + threadIdx.x;
   if (i >= n) return;
