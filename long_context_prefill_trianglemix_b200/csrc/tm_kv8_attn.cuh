@@ -54,6 +54,8 @@ struct AttnP {
   float* part_o;      // [2 grid][8 NT][D]
   float2* part_ml;    // [2 grid][8 NT]
   float* warp_o;      // [grid][warps][8 NT][D]: a warp's first partial
+  int4* close;        // [grid]: the item from an earlier CTA that ends in this one (item, first CTA,
+                      // its slot, last CTA), or -1
   float* lse;         // [items][8 NT] (log2), +inf where a row keeps nothing
   float* scores;      // [items][cap][8 NT] (log2), or null
   int grid;
@@ -67,6 +69,28 @@ __device__ __forceinline__ int clamp_len(const AttnP& p, int b) {
 __device__ __forceinline__ int parts_of(long long T, int grid) {
   const long long most = (T + kAttnWarps - 1) / kAttnWarps;
   return static_cast<int>(most < grid ? (most < 1 ? 1 : most) : grid);
+}
+
+// Where every item is short, at most two warps' shares, none is cut: a boundary that
+// falls inside one moves to its start. (Among long items that would unbalance the
+// warps: 24 sequences of 327 to 32768 tokens took 57 us so, 51 us cut evenly.)
+__device__ __forceinline__ bool whole_items(long long T, int grid, int longest) {
+  return longest * static_cast<long long>(grid) * kAttnWarps <= 2 * T || longest <= 2;
+}
+
+__device__ __forceinline__ int sequence_of(const int* pre, int B, int x) {
+  int lo = 0, hi = B;  // the last b with pre[b] <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int item_start(const AttnP& p, const int* pre, int x) {
+  if (x >= pre[p.a.B]) return x;
+  const int b = sequence_of(pre, p.a.B, x);
+  return x - (x - pre[b]) % ((pre[b + 1] - pre[b]) / p.items_per_b);
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -137,11 +161,7 @@ __device__ __forceinline__ UnitAt locate(const AttnP& p, const int* pre, int x, 
   at.item = -1; at.u = 0; at.row = -1;
   at.kr = at.vr = 0.f;
   if (x >= xe) return at;
-  int lo = 0, hi = p.a.B;  // the last b with pre[b] <= x
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= x) lo = mid; else hi = mid;
-  }
+  const int lo = sequence_of(pre, p.a.B, x);
   const int U = (pre[lo + 1] - pre[lo]) / p.items_per_b;
   const int it = (x - pre[lo]) / U;
   at.u = x - pre[lo] - it * U;
@@ -151,20 +171,30 @@ __device__ __forceinline__ UnitAt locate(const AttnP& p, const int* pre, int x, 
   if (static_cast<unsigned>(page) < static_cast<unsigned>(p.a.c.num_pages)) {
     const long long block = static_cast<long long>(page) * p.a.c.Hkv + it / p.RT;
     at.row = static_cast<int>(((block << p.page_log) + (tok0 & (p.a.c.page - 1))) / (128 / D));
-    at.kr = __ldg(p.a.c.k_range + block);
-    at.vr = __ldg(p.a.c.v_range + block);
   }
   return at;
 }
 
-// Prefix sums of the sequences' units (times items per sequence) in shared memory.
-__device__ __forceinline__ void unit_prefix(const AttnP& p, int* pre) {
-  __shared__ int s_warp[kAttnWarps];
+template <int D>
+__device__ __forceinline__ void load_ranges(const AttnP& p, UnitAt& at) {
+  if (at.row < 0) return;
+  const long long block = (static_cast<long long>(at.row) * (128 / D)) >> p.page_log;
+  at.kr = __ldg(p.a.c.k_range + block);
+  at.vr = __ldg(p.a.c.v_range + block);
+}
+
+// Prefix sums of the sequences' units (times items per sequence) in shared memory;
+// returns the units of the longest.
+__device__ __forceinline__ int unit_prefix(const AttnP& p, int* pre) {
+  __shared__ int s_warp[kAttnWarps], s_most[kAttnWarps];
+  int most = 0;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   int carry = 0;
   for (int b0 = 0; b0 < p.a.B; b0 += kAttnThreads) {
     const int b = b0 + t;
-    int x = b < p.a.B ? (clamp_len(p, b) + kUnit - 1) / kUnit * p.items_per_b : 0;
+    const int U = b < p.a.B ? (clamp_len(p, b) + kUnit - 1) / kUnit : 0;
+    most = max(most, U);
+    int x = U * p.items_per_b;
     const int own = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -181,8 +211,13 @@ __device__ __forceinline__ void unit_prefix(const AttnP& p, int* pre) {
     if (b < p.a.B) pre[b] = before + x - own;
     __syncthreads();
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) s_most[w] = most;
   if (t == 0) pre[p.a.B] = carry;
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAttnWarps; ++i) most = max(most, s_most[i]);
+  return most;
 }
 
 __device__ __forceinline__ void store_bf16(uint16_t* dst, float a, float b) {
@@ -221,20 +256,55 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   if (lane == 0)
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
   if (lane == 0) fence_barrier_init();
-  unit_prefix(p, pre);
+  const int longest = unit_prefix(p, pre);
   const long long T = pre[a.B];
   const int parts = parts_of(T, p.grid), cta = blockIdx.x;
-  if (cta >= parts) return;
-  const int cs = static_cast<int>(T * cta / parts), ce = static_cast<int>(T * (cta + 1) / parts);
-  const int xs = cs + static_cast<int>(static_cast<long long>(ce - cs) * warp / kAttnWarps);
-  const int xe = cs + static_cast<int>(static_cast<long long>(ce - cs) * (warp + 1) / kAttnWarps);
+  for (int z = cta; z < a.B; z += gridDim.x) {  // sequences without tokens: zeros
+    if (pre[z + 1] != pre[z]) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
+                                        static_cast<long long>(z) * a.nq * a.Hq * D);
+    for (int i = tid; i < a.nq * a.Hq * (D / 8); i += kAttnThreads) o[i] = make_uint4(0, 0, 0, 0);
+  }
+  if (cta >= parts) {
+    if (tid == 0) p.close[cta] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  // the CTA's part [cs, ce) and this warp's [xs, xe): lanes 0, 1, 2, 3 look up one bound each
+  const bool whole = whole_items(T, p.grid, longest);
+  int cs, ce, xs, xe;
+  {
+    const int c0 = static_cast<int>(T * cta / parts), c1 = static_cast<int>(T * (cta + 1) / parts);
+    const long long w = warp + (lane & 1);
+    const int x = (lane & 2) ? c0 + static_cast<int>((c1 - c0) * w / kAttnWarps)
+                             : (lane & 1) ? c1 : c0;
+    const int at = whole ? item_start(p, pre, x) : x;
+    cs = __shfl_sync(0xffffffffu, at, 0);
+    ce = __shfl_sync(0xffffffffu, at, 1);
+    xs = __shfl_sync(0xffffffffu, at, 2);
+    xe = __shfl_sync(0xffffffffu, at, 3);
+  }
+  if (tid == 0) {
+    // does the item that holds the part's first unit begin before it and end in it?
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (ce > cs && item_start(p, pre, cs) < cs) {
+      const int sb = sequence_of(pre, a.B, cs), U0 = item_start(p, pre, cs);
+      const int U = (pre[sb + 1] - pre[sb]) / p.items_per_b;
+      if (U0 + U <= ce) {
+        // the part that holds unit U0: the last c with floor(c T / parts) <= U0
+        const int c0 = static_cast<int>(((U0 + 1LL) * parts - 1) / T);
+        rec = make_int4(sb * p.items_per_b + (U0 - pre[sb]) / U, c0, 2 * c0 + (T * c0 / parts < U0),
+                        cta);
+      }
+    }
+    p.close[cta] = rec;
+  }
   const int n_units = xe - xs;
   const float s_unit = a.scale * 1.4426950408889634f / full<FMT>();
   uint8_t* ring = smem + warp * C::kWarpRing;
   const uint32_t ring_addr = smem_addr(ring);
 
   // Lane i & 31 holds where unit i lies; the next 32 are looked up a batch ahead.
-  UnitAt cur = locate<D>(p, pre, xs + lane, xe), nxt = locate<D>(p, pre, xs + 32 + lane, xe);
+  UnitAt cur = locate<D>(p, pre, xs + lane, xe), nxt = cur;
   auto issue = [&](int i, int batch) {
     if (i >= n_units || lane != (i & 31)) return;
     const int row = (i >> 5) == batch ? cur.row : nxt.row;
@@ -249,6 +319,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     tma_load_2d(ring_addr + st * 2 * C::kHalf + C::kHalf, &tv, bar, 0, row);
   };
   for (int i = 0; i < S - 1; ++i) issue(i, 0);
+  load_ranges<D>(p, cur);
+  nxt = locate<D>(p, pre, xs + 32 + lane, xe);
+  load_ranges<D>(p, nxt);
 
   // Byte offsets of this thread's rows in a unit. K: tokens g and g + 8, 16-byte
   // chunks 2t, 2t + 1 (D = 128) or t; V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, D / 8
@@ -286,6 +359,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     if ((i & 31) == 0 && i > 0) {
       cur = nxt;
       nxt = locate<D>(p, pre, xs + i + 32 + lane, xe);
+      load_ranges<D>(p, nxt);
     }
     const int next_item = i < n_units ? __shfl_sync(0xffffffffu, cur.item, i & 31) : -1;
     if (next_item != item) {
@@ -306,9 +380,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
             for (int e = 0; e < 2; ++e) {
               const int rr = row0 + 8 * n + 2 * t + e;
               const bool some = l[n][e] != 0.f;
-              if (p.lse && g == 0)
+              if (p.lse && g == 0)  // rows past the last one weigh nothing
                 p.lse[static_cast<long long>(item) * (8 * NT) + 8 * n + 2 * t + e] =
-                    some ? ref[n][e] - kLift + log2f(l[n][e]) : INFINITY;
+                    some && rr < p.rows ? ref[n][e] - kLift + log2f(l[n][e]) : INFINITY;
               if (rr >= p.rows) continue;
               const float inv = some ? 1.f / l[n][e] : 0.f;
               uint16_t* dst = out_row<D>(p, b, h, rr) + g * (D / 8);
@@ -383,7 +457,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
         for (int e = 0; e < 2; ++e) {
           sc[n][e] = __shfl_sync(0xffffffffu, row_sc, 4 * (2 * t + e));
           const int rr = row0 + 8 * n + 2 * t + e;
-          lim[n][e] = rr < p.rows ? len - a.nq + rr / p.G : -1;  // last key of the row
+          lim[n][e] = len - a.nq + min(rr, p.rows - 1) / p.G;  // last key of the row
           ref[n][e] = kLowest;
           l[n][e] = 0.f;
         }
@@ -436,7 +510,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       }
     }
     // keys up to len - nq are seen by every row
-    const bool edge = tok0 + kUnit - 1 > len - a.nq || !there || p.rows - row0 < 8 * NT;
+    const bool edge = tok0 + kUnit - 1 > len - a.nq || !there;
     uint32_t pb[NT][2];
     float vf[NT][2];
     if (edge) {  // bytes behind the last token may hold anything, NaN codes among it
@@ -526,115 +600,136 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   __syncthreads();
   if (*abort_flag) return;
 
-  // Join the warps' partials of each item, in order.
-  for (int s0 = 0; s0 < 2 * kAttnWarps;) {
-    const int item = s_item[s0];
-    if (item < 0) {
-      ++s0;
-      continue;
-    }
-    int s1 = s0 + 1;
-    while (s1 < 2 * kAttnWarps && (s_item[s1] < 0 || s_item[s1] == item)) ++s1;
-    const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
-    const int U = (pre[ib + 1] - pre[ib]) / p.items_per_b, h = it / p.RT, rt = it - h * p.RT;
-    const int U0 = pre[ib] + it * U;
-    const bool whole = cs <= U0 && U0 + U <= ce;
-    const int slot = 2 * cta + (U0 > cs);
-    for (int i = tid; i < 8 * NT * (D / 4); i += kAttnThreads) {
-      const int c = i / (D / 4), d4 = i - c * (D / 4);
-      float m = kLowest;
-      for (int s = s0; s < s1; ++s)
-        if (s_item[s] == item) m = fmaxf(m, s_ml[s * 8 * NT + c].x);
-      float ls = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = s0; s < s1; ++s) {
-        if (s_item[s] != item) continue;
-        const float2 ml = s_ml[s * 8 * NT + c];
-        const float f = ex2(ml.x - m);
-        const float* src = s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kWarpRing)
-                                 : p.warp_o + (static_cast<long long>(cta) * kAttnWarps + (s >> 1)) *
-                                                  8 * NT * D;
-        const float4 v = *reinterpret_cast<const float4*>(src + c * D + 4 * d4);
-        ls += ml.y * f;
-        o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+  // Join the warps' partials of each item, in order. A warp takes one column (row of
+  // the item) of one item at a time, D / 4 lanes a column; the loads of all its
+  // partials go out together.
+  constexpr int kSlots = 2 * kAttnWarps, kLanes = D / 4, kCols = 32 / kLanes;
+  int it_of[kSlots];
+#pragma unroll
+  for (int k = 0; k < kSlots / 4; ++k) {
+    const int4 v = reinterpret_cast<const int4*>(s_item)[k];
+    it_of[4 * k] = v.x; it_of[4 * k + 1] = v.y; it_of[4 * k + 2] = v.z; it_of[4 * k + 3] = v.w;
+  }
+  uint32_t first = 0;  // slots that begin an item
+  {
+    int last = -1;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      if (it_of[k] >= 0 && it_of[k] != last) {
+        first |= 1u << k;
+        last = it_of[k];
       }
-      if (whole) {
-        const int rr = rt * 8 * NT + c;
-        const bool some = ls != 0.f;
-        if (p.lse && d4 == 0)
-          p.lse[static_cast<long long>(item) * (8 * NT) + c] =
-              some ? m - kLift + log2f(ls) : INFINITY;
-        if (rr < p.rows) {
-          const float inv = some ? 1.f / ls : 0.f;
-          uint16_t* dst = out_row<D>(p, ib, h, rr) + 4 * d4;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(sm100::pack_bf16x2(o.x * inv, o.y * inv),
-                                                      sm100::pack_bf16x2(o.z * inv, o.w * inv));
+    }
+  }
+  const int tasks = __popc(first) * (8 * NT / kCols), sub = lane / kLanes, d4 = lane % kLanes;
+  for (int task = warp; task < tasks; task += kAttnWarps) {
+    const int c = (task % (8 * NT / kCols)) * kCols + sub;
+    uint32_t f = first;
+    for (int k = task / (8 * NT / kCols); k > 0; --k) f &= f - 1;
+    const int s0 = __ffs(f) - 1;
+    int it_id = 0;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k)
+      if (k == s0) it_id = it_of[k];
+    float2 ml[kSlots];
+    float m = kLowest;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      ml[k] = make_float2(kLowest, 0.f);
+      if (it_of[k] == it_id) ml[k] = s_ml[k * 8 * NT + c];
+    }
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) m = fmaxf(m, ml[k].x);
+    float ls = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k0 = 0; k0 < kSlots; k0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int s = k0 + k;
+        if (it_of[s] == it_id) {
+          const float* src = s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kWarpRing)
+                                   : p.warp_o + (static_cast<long long>(cta) * kAttnWarps + (s >> 1)) *
+                                                    8 * NT * D;
+          v[k] = *reinterpret_cast<const float4*>(src + c * D + 4 * d4);
         }
-      } else {
-        reinterpret_cast<float4*>(p.part_o)[(static_cast<long long>(slot) * 8 * NT + c) * (D / 4) + d4] = o;
-        if (d4 == 0) p.part_ml[static_cast<long long>(slot) * 8 * NT + c] = make_float2(m, ls);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = ex2(ml[k0 + k].x - m);
+        ls += ml[k0 + k].y * w;
+        o.x += v[k].x * w; o.y += v[k].y * w; o.z += v[k].z * w; o.w += v[k].w * w;
       }
     }
-    s0 = s1;
+    const int ib = it_id / p.items_per_b, it = it_id - ib * p.items_per_b;
+    const int U = (pre[ib + 1] - pre[ib]) / p.items_per_b;
+    const int U0 = pre[ib] + it * U;
+    if (cs <= U0 && U0 + U <= ce) {
+      const int hh = it / p.RT, rr = (it - hh * p.RT) * 8 * NT + c;
+      const bool some = ls != 0.f;
+      if (p.lse && d4 == 0)
+        p.lse[static_cast<long long>(it_id) * (8 * NT) + c] =
+            some && rr < p.rows ? m - kLift + log2f(ls) : INFINITY;
+      if (rr < p.rows) {
+        const float inv = some ? 1.f / ls : 0.f;
+        *reinterpret_cast<uint2*>(out_row<D>(p, ib, hh, rr) + 4 * d4) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      }
+    } else {
+      const long long at = static_cast<long long>(2 * cta + (U0 > cs)) * 8 * NT + c;
+      reinterpret_cast<float4*>(p.part_o)[at * kLanes + d4] = o;
+      if (d4 == 0) p.part_ml[at] = make_float2(m, ls);
+    }
   }
 }
 
-// One CTA per (item, row): joins the partials of an item that was cut between
-// CTAs, in their order; writes the zeros of a sequence without tokens.
+// One CTA per (CTA of the main kernel, row): joins the partials of the item that was
+// cut and ended in that CTA, in their order.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
   constexpr int V = D / 4, GR = 128 / V;  // float4 lanes of a row, groups of partials
-  const int item = blockIdx.x, c = blockIdx.y, t = threadIdx.x;
-  const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
-  const int h = it / p.RT, rt = it - h * p.RT, rr = rt * 8 * NT + c;
-  long long before = 0, T = 0;
-  for (int b = t; b < p.a.B; b += 128) {
-    const long long x = (clamp_len(p, b) + kUnit - 1) / kUnit;
-    T += x;
-    if (b < ib) before += x;
-  }
-  __shared__ long long s_sum[2][4];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    T += __shfl_xor_sync(0xffffffffu, T, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if ((t & 31) == 0) { s_sum[0][t >> 5] = T; s_sum[1][t >> 5] = before; }
-  __syncthreads();
-  T = (s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * p.items_per_b;
-  const int U = (clamp_len(p, ib) + kUnit - 1) / kUnit;
-  const long long U0 = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * p.items_per_b +
-                       static_cast<long long>(it) * U;
-  const int lane4 = t % V, grp = t / V;
-  // What is above reads only lens. The rest reads what the kernel before wrote, or
-  // may be read by work that follows this launch.
+  const int c = blockIdx.y, t = threadIdx.x, lane4 = t % V, grp = t / V;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (U == 0) {
-    if (rr < p.rows && grp == 0)
-      *reinterpret_cast<uint2*>(out_row<D>(p, ib, h, rr) + 4 * lane4) = make_uint2(0, 0);
-    return;
-  }
-  const int parts = parts_of(T, p.grid);
-  // part of unit x: the last c with floor(c T / parts) <= x
-  const int c0 = static_cast<int>(((U0 + 1) * parts - 1) / T);
-  const int c1 = static_cast<int>(((U0 + U) * parts - 1) / T);
-  if (c0 == c1) return;
-  const int first = 2 * c0 + (T * c0 / parts < U0);
+  const int4 rec = p.close[blockIdx.x];
+  if (rec.x < 0) return;
+  const int item = rec.x, c0 = rec.y, first = rec.z, c1 = rec.w;
+  const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
+  const int h = it / p.RT, rt = it - h * p.RT, rr = rt * 8 * NT + c;
   __shared__ float4 s_o[GR][V];
   __shared__ float2 s_ml[GR];
-  float m = kLowest;
-  for (int k = c0 + grp; k <= c1; k += GR)
-    m = fmaxf(m, p.part_ml[static_cast<long long>(k == c0 ? first : 2 * k) * 8 * NT + c].x);
+  float m = kLowest, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int k = c0 + grp; k <= c1; k += GR) {
-    const long long at = static_cast<long long>(k == c0 ? first : 2 * k) * 8 * NT + c;
-    const float2 ml = p.part_ml[at];
-    const float4 v = reinterpret_cast<const float4*>(p.part_o)[at * V + lane4];
-    const float f = ex2(ml.x - m);
-    l += ml.y * f;
-    o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+  constexpr int kAhead = 4;  // partials a thread loads at once
+  for (int k0 = c0 + grp; k0 <= c1; k0 += GR * kAhead) {
+    float2 ml[kAhead];
+    float4 v[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int k = k0 + x * GR;
+      const long long at = static_cast<long long>(k == c0 ? first : 2 * k) * 8 * NT + c;
+      ml[x] = make_float2(kLowest, 0.f);
+      v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k <= c1) {
+        ml[x] = p.part_ml[at];
+        v[x] = reinterpret_cast<const float4*>(p.part_o)[at * V + lane4];
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) mn = fmaxf(mn, ml[x].x);
+    const float f0 = ex2(m - mn);
+    m = mn;
+    l *= f0;
+    o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const float f = ex2(ml[x].x - m);
+      l += ml[x].y * f;
+      o.x += v[x].x * f; o.y += v[x].y * f; o.z += v[x].z * f; o.w += v[x].w * f;
+    }
   }
   s_o[grp][lane4] = o;
   if (lane4 == 0) s_ml[grp] = make_float2(m, l);
@@ -654,7 +749,7 @@ __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
   }
   const bool some = l != 0.f;
   if (p.lse && lane4 == 0)
-    p.lse[static_cast<long long>(item) * (8 * NT) + c] = some ? m - kLift + log2f(l) : INFINITY;
+    p.lse[static_cast<long long>(item) * (8 * NT) + c] = some && rr < p.rows ? m - kLift + log2f(l) : INFINITY;
   if (rr >= p.rows) return;
   const float inv = some ? 1.f / l : 0.f;
   *reinterpret_cast<uint2*>(out_row<D>(p, ib, h, rr) + 4 * lane4) =
@@ -686,7 +781,7 @@ __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
 
 struct AttnLayout {
   int NT, RT;
-  long long part_o, part_ml, warp_o, lse, scores, total;
+  long long part_o, part_ml, warp_o, close, lse, scores, total;
 };
 
 AttnLayout attn_layout(int B, int nq, int Hq, int Hkv, int D, int max_pages, int page,
@@ -701,7 +796,8 @@ AttnLayout attn_layout(int B, int nq, int Hq, int Hkv, int D, int max_pages, int
   l.part_o = 0;
   l.part_ml = al(slots * D * 4);
   l.warp_o = l.part_ml + al(slots * 8);
-  l.lse = l.warp_o + al(slots / 2 * kAttnWarps * D * 4);
+  l.close = l.warp_o + al(slots / 2 * kAttnWarps * D * 4);
+  l.lse = l.close + al(2LL * kMaxSms * 16);
   l.scores = l.lse + (with_weights ? al(items * 8 * l.NT * 4) : 0);
   l.total = l.scores + (with_weights ? al(items * 8 * l.NT * max_pages * page * 4) : 0);
   return l;
@@ -733,9 +829,12 @@ int attn_run(AttnP& p, DeviceInfo* di) {
   CUtensorMap tk, tv;
   if (encode_codes<D>(&tk, a.c.k8, a.c) || encode_codes<D>(&tv, a.c.v8, a.c)) return TM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-  p.grid = std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1);
+  // a CTA for every unit a warp could get, at most what is resident at once
+  const long long units = static_cast<long long>(a.B) * p.items_per_b * ((p.cap + kUnit - 1) / kUnit);
+  p.grid = static_cast<int>(std::min<long long>(std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1),
+                                                (units + kAttnWarps - 1) / kAttnWarps));
   attn_kernel8<D, FMT, NT><<<p.grid, kAttnThreads, C::kSmem + a.B * 4, st>>>(tk, tv, p);
-  const dim3 grid(static_cast<unsigned>(a.B * p.items_per_b), 8 * NT);
+  const dim3 grid(p.grid, 8 * NT);
   if (launch_early(combine_kernel<D, NT>, grid, 128, 0, st, p)) return TM_ERR_CUDA;
   if (!p.scores) return counted(2);
   const long long want = (p.cap + 1023) / 1024;
@@ -774,6 +873,7 @@ int launch_kv8_attn(const Kv8AttnArgs& a) {
   p.part_o = reinterpret_cast<float*>(ws + l.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   p.warp_o = reinterpret_cast<float*>(ws + l.warp_o);
+  p.close = reinterpret_cast<int4*>(ws + l.close);
   p.lse = a.weights ? reinterpret_cast<float*>(ws + l.lse) : nullptr;
   p.scores = a.weights ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
   if (a.c.D == 128)
