@@ -57,7 +57,8 @@ struct AttnP {
   int4* close;        // [grid]: the item from an earlier CTA that ends in this one (item, first CTA,
                       // its slot, last CTA), or -1
   float* lse;         // [items][8 NT] (log2), +inf where a row keeps nothing
-  float* scores;      // [items][cap][8 NT] (log2), or null
+  float* scores;      // [items][cap][rs] (log2), or null
+  int rs;             // rows kept of a token's scores: those of an item, to a multiple of 4
   int grid;
 };
 
@@ -137,7 +138,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& first, uint32_t& sec
 // rows, 128-byte swizzled by the TMA load).
 template <int D, int NT>
 struct AttnCfg {
-  static constexpr int S = (NT == 1 ? 3 : 6) * (D == 64 ? 2 : 1);
+  // One unit loads while another is computed. More in flight is slower: 3 deep, 8 sequences
+  // of 131072 tokens took 347 us, 2 deep 324 us.
+  static constexpr int S = D == 64 ? (NT == 1 ? 4 : 3) : 2;
   static constexpr int kHalf = kUnit * D;  // bytes of a unit's K or V
   static constexpr int kWarpRing = S * 2 * kHalf;
   static constexpr int kMl = kAttnWarps * kWarpRing;  // float2 [2 warps][8 NT]
@@ -283,21 +286,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     xs = __shfl_sync(0xffffffffu, at, 2);
     xe = __shfl_sync(0xffffffffu, at, 3);
   }
-  if (tid == 0) {
-    // does the item that holds the part's first unit begin before it and end in it?
-    int4 rec = make_int4(-1, 0, 0, 0);
-    if (ce > cs && item_start(p, pre, cs) < cs) {
-      const int sb = sequence_of(pre, a.B, cs), U0 = item_start(p, pre, cs);
-      const int U = (pre[sb + 1] - pre[sb]) / p.items_per_b;
-      if (U0 + U <= ce) {
-        // the part that holds unit U0: the last c with floor(c T / parts) <= U0
-        const int c0 = static_cast<int>(((U0 + 1LL) * parts - 1) / T);
-        rec = make_int4(sb * p.items_per_b + (U0 - pre[sb]) / U, c0, 2 * c0 + (T * c0 / parts < U0),
-                        cta);
-      }
-    }
-    p.close[cta] = rec;
-  }
   const int n_units = xe - xs;
   const float s_unit = a.scale * 1.4426950408889634f / full<FMT>();
   uint8_t* ring = smem + warp * C::kWarpRing;
@@ -322,6 +310,21 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   load_ranges<D>(p, cur);
   nxt = locate<D>(p, pre, xs + 32 + lane, xe);
   load_ranges<D>(p, nxt);
+  if (tid == 0) {
+    // does the item that holds the part's first unit begin before it and end in it?
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (ce > cs && item_start(p, pre, cs) < cs) {
+      const int sb = sequence_of(pre, a.B, cs), U0 = item_start(p, pre, cs);
+      const int U = (pre[sb + 1] - pre[sb]) / p.items_per_b;
+      if (U0 + U <= ce) {
+        // the part that holds unit U0: the last c with floor(c T / parts) <= U0
+        const int c0 = static_cast<int>(((U0 + 1LL) * parts - 1) / T);
+        rec = make_int4(sb * p.items_per_b + (U0 - pre[sb]) / U, c0, 2 * c0 + (T * c0 / parts < U0),
+                        cta);
+      }
+    }
+    p.close[cta] = rec;
+  }
 
   // Byte offsets of this thread's rows in a unit. K: tokens g and g + 8, 16-byte
   // chunks 2t, 2t + 1 (D = 128) or t; V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, D / 8
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       h = it / p.RT;
       row0 = (it - h * p.RT) * 8 * NT;
       len = clamp_len(p, b);
-      scores = p.scores ? p.scores + static_cast<long long>(item) * p.cap * (8 * NT) : nullptr;
+      scores = p.scores ? p.scores + static_cast<long long>(item) * p.cap * p.rs : nullptr;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = row0 + 8 * n + g;
@@ -478,11 +481,12 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     const int tok0 = u * kUnit;
     ++u;
     const uint8_t* stage = ring + (i % S) * 2 * C::kHalf;
-    float s[NT][4];
+    // two accumulators a row tile (even and odd steps): half the chain of dependent MMAs
+    float s[NT][4], s2[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const uint4 ka = *reinterpret_cast<const uint4*>(stage + (k_off[0] ^ (j << 4)));
@@ -495,7 +499,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
         widen<FMT>(k1[w], a1, a3);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          mma16816(s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], s[n]);
+          if (w & 1)
+            mma16816(s2[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], s2[n]);
+          else
+            mma16816(s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], s[n]);
       }
     }
     uint32_t v[4][D / 32];
@@ -524,7 +531,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float f0 = sc[n][0] * kr, f1 = sc[n][1] * kr;
-      s[n][0] *= f0; s[n][1] *= f1; s[n][2] *= f0; s[n][3] *= f1;
+      s[n][0] = (s[n][0] + s2[n][0]) * f0;
+      s[n][1] = (s[n][1] + s2[n][1]) * f1;
+      s[n][2] = (s[n][2] + s2[n][2]) * f0;
+      s[n][3] = (s[n][3] + s2[n][3]) * f1;
       vf[n][0] = vf[n][1] = vr * (1.f / full<FMT>());
       if (edge) {
         // tokens of the unit that each of the thread's rows sees
@@ -537,11 +547,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
         if (see0 <= 0) vf[n][0] = 0.f;
         if (see1 <= 0) vf[n][1] = 0.f;
       }
-      if (scores) {
-        float* at = scores + (static_cast<long long>(tok0) + g) * (8 * NT) + 8 * n + 2 * t;
+      if (scores && 8 * n + 2 * t < p.rs) {
+        float* at = scores + (static_cast<long long>(tok0) + g) * p.rs + 8 * n + 2 * t;
         if (tok0 + g < len) *reinterpret_cast<float2*>(at) = make_float2(s[n][0], s[n][1]);
         if (tok0 + g + 8 < len)
-          *reinterpret_cast<float2*>(at + 64 * NT) = make_float2(s[n][2], s[n][3]);
+          *reinterpret_cast<float2*>(at + 8 * p.rs) = make_float2(s[n][2], s[n][3]);
       }
       const float over = fmaxf(fmaxf(s[n][0], s[n][2]) - ref[n][0],
                                fmaxf(s[n][1], s[n][3]) - ref[n][1]);
@@ -766,10 +776,11 @@ __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
     float w = 0.f;
     for (int rt = 0; rt < p.RT; ++rt) {
       const long long item = static_cast<long long>(b) * p.items_per_b + h * p.RT + rt;
-      const float4* s = reinterpret_cast<const float4*>(p.scores + (item * p.cap + j) * (8 * NT));
+      const float4* s = reinterpret_cast<const float4*>(p.scores + (item * p.cap + j) * p.rs);
       const float4* z = reinterpret_cast<const float4*>(p.lse + item * (8 * NT));
 #pragma unroll
       for (int n = 0; n < 2 * NT; ++n) {
+        if (4 * n >= p.rs) break;
         const float4 x = s[n], y = z[n];
         w += (ex2(x.x - y.x) + ex2(x.y - y.y)) + (ex2(x.z - y.z) + ex2(x.w - y.w));
       }
@@ -780,7 +791,7 @@ __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
 }
 
 struct AttnLayout {
-  int NT, RT;
+  int NT, RT, rs;
   long long part_o, part_ml, warp_o, close, lse, scores, total;
 };
 
@@ -799,7 +810,8 @@ AttnLayout attn_layout(int B, int nq, int Hq, int Hkv, int D, int max_pages, int
   l.close = l.warp_o + al(slots / 2 * kAttnWarps * D * 4);
   l.lse = l.close + al(2LL * kMaxSms * 16);
   l.scores = l.lse + (with_weights ? al(items * 8 * l.NT * 4) : 0);
-  l.total = l.scores + (with_weights ? al(items * 8 * l.NT * max_pages * page * 4) : 0);
+  l.rs = (std::min(rows, 8 * l.NT) + 3) / 4 * 4;
+  l.total = l.scores + (with_weights ? al(items * l.rs * max_pages * page * 4) : 0);
   return l;
 }
 
@@ -867,6 +879,7 @@ int launch_kv8_attn(const Kv8AttnArgs& a) {
   p.G = a.Hq / a.c.Hkv;
   p.rows = a.nq * p.G;
   p.RT = l.RT;
+  p.rs = l.rs;
   p.items_per_b = a.c.Hkv * l.RT;
   p.page_log = a.c.page == 16 ? 4 : a.c.page == 32 ? 5 : a.c.page == 64 ? 6 : 7;
   p.cap = static_cast<long long>(a.max_pages) * a.c.page;

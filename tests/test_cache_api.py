@@ -149,7 +149,7 @@ def test_attention_refusals():
     assert size(2, 1, 4, 3, 64, 4, 16, 0, ctypes.byref(n)) == INVALID
     assert size(2, 1, 4, 2, 80, 4, 16, 0, ctypes.byref(n)) == UNSUPPORTED
     plain = tm.tm_kv8_attn_workspace_size(2, 1, 4, 2, 64, 4, 16, False)
-    scores = 2 * 2 * 8 * 64 * 4  # items, padded rows, tokens, fp32
+    scores = 2 * 2 * 4 * 64 * 4  # items, padded rows, tokens, fp32
     assert tm.tm_kv8_attn_workspace_size(2, 1, 4, 2, 64, 4, 16, True) >= plain + scores
     assert call("tm_kv8_attn_fwd", ATTN, workspace_bytes=plain - 1) == INVALID
 
