@@ -1700,12 +1700,30 @@ struct WtLayout {
   int tpt, nqt, nkt, splits, q_group;
   long long lse, total;
 };
-// A tiles an item takes: four share each B tile and keep an SM's four warpgroups busy;
-// fewer where that would leave SMs without an item (8 key rows of 33 tiles: 46 us of four, 39 of one).
-int weights_group(long long bg, int tiles) {
-  int g = kWtTiles;
-  while (g > 1 && bg * ((tiles + g - 1) / g) < 148) g /= 2;
-  return g;
+// Time of one B tile against g A tiles (us, measured with 4 to 28 B tiles an item): four
+// share each B tile and keep an SM's four warpgroups busy, one leaves three idle but
+// gives work to more SMs.
+double weights_round(int g) { return g == 1 ? 0.95 : g == 2 ? 1.3 : 2.3; }
+
+// The A tiles an item takes and the parts that the B tiles are cut into (1 in pass 2)
+// for the shortest run of `bg` x `a_tiles` x `b_tiles` on 148 SMs, by that time, a
+// fixed cost an item, and the waves of items.
+void weights_shape(long long bg, int a_tiles, int b_tiles, bool cut, int* group, int* splits) {
+  double best = 1e300;
+  for (int g = 1; g <= kWtTiles; g *= 2) {
+    if (g > 1 && g / 2 >= a_tiles) break;
+    const long long groups = bg * ((a_tiles + g - 1) / g);
+    const long long most = cut ? std::min<long long>(b_tiles, (148 * 8 + groups - 1) / groups) : 1;
+    for (long long s = 1; s <= most; ++s) {
+      const long long waves = (groups * s + 147) / 148;
+      const double t = waves * (((b_tiles + s - 1) / s) * weights_round(g) + 1.5);
+      if (t < best * 0.999) {
+        best = t;
+        *group = g;
+        *splits = static_cast<int>(s);
+      }
+    }
+  }
 }
 
 WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
@@ -1715,24 +1733,7 @@ WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
   l.tpt = 128 / G;
   l.nqt = (rows + l.tpt - 1) / l.tpt;
   l.nkt = (N + BN - 1) / BN;
-  // Pass 1 cuts the key range until there are about four items an SM, of four
-  // key tiles or more. The count is fixed so that a workspace's size is.
-  // Among the counts from there to twice that, the one whose last wave on 148 SMs is fullest.
-  const long long bg = static_cast<long long>(B) * Hkv;
-  l.q_group = std::min(kWtTiles, l.nqt >= 4 ? 4 : l.nqt >= 2 ? 2 : 1);
-  const long long groups = bg * ((l.nqt + l.q_group - 1) / l.q_group);
-  const long long most = std::max(1, (l.nkt + 3) / 4);
-  const long long base = std::max(1LL, std::min<long long>((592 + groups - 1) / groups, most));
-  double best = 0.0;
-  l.splits = static_cast<int>(base);
-  for (long long x = base; base > 1 && x <= std::min(2 * base, most); ++x) {
-    const long long items = groups * x, waves = (items + 147) / 148;
-    const double fill = static_cast<double>(items) / (waves * 148);
-    if (fill > best + 1e-9) {
-      best = fill;
-      l.splits = static_cast<int>(x);
-    }
-  }
+  weights_shape(static_cast<long long>(B) * Hkv, l.nqt, l.nkt, true, &l.q_group, &l.splits);
   const long long tile_rows = static_cast<long long>(B) * Hkv * l.nqt * 128;
   l.lse = al(tile_rows * l.splits * 8);
   l.total = l.lse + al(tile_rows * 4);
@@ -1779,7 +1780,8 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
   const long long rows = bg * l.nqt * 128;
   if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), 256, 0, st, p))
     return TM_ERR_CUDA;
-  p.group = weights_group(bg, l.nkt);
+  int one = 1;
+  weights_shape(bg, l.nkt, l.nqt, false, &p.group, &one);
   p.items = static_cast<int>(bg * ((l.nkt + p.group - 1) / p.group));
   if (launch_early(weights_kernel<D, 2>, dim3(std::min<unsigned>(p.items, sms)), kWtThreads, C::kSmem,
                    st, tq, tk, p))
