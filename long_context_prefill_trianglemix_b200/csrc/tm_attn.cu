@@ -1700,10 +1700,13 @@ struct WtLayout {
   int tpt, nqt, nkt, splits, q_group;
   long long lse, total;
 };
-// Time of one B tile against g A tiles (us, measured with 4 to 28 B tiles an item): four
-// share each B tile and keep an SM's four warpgroups busy, one leaves three idle but
-// gives work to more SMs.
-double weights_round(int g) { return g == 1 ? 0.95 : g == 2 ? 1.3 : 2.3; }
+// Time of nb B tiles against g A tiles (us, measured): rounds of four (B tile, A tile)
+// products for the four warpgroups, the last one by how many it occupies.
+double weights_time(int g, int nb) {
+  const double t[5] = {0.0, 0.95, 1.3, 1.8, 2.3};
+  const int phases = kWtTiles / g;
+  return (nb / phases) * t[4] + t[(nb % phases) * g];
+}
 
 // The A tiles an item takes and the parts that the B tiles are cut into (1 in pass 2)
 // for the shortest run of `bg` x `a_tiles` x `b_tiles` on 148 SMs, by that time, a
@@ -1716,7 +1719,7 @@ void weights_shape(long long bg, int a_tiles, int b_tiles, bool cut, int* group,
     const long long most = cut ? std::min<long long>(b_tiles, (148 * 8 + groups - 1) / groups) : 1;
     for (long long s = 1; s <= most; ++s) {
       const long long waves = (groups * s + 147) / 148;
-      const double t = waves * (((b_tiles + s - 1) / s) * weights_round(g) + 1.5);
+      const double t = waves * (weights_time(g, static_cast<int>((b_tiles + s - 1) / s)) + 1.5);
       if (t < best * 0.999) {
         best = t;
         *group = g;
@@ -1735,7 +1738,7 @@ WtLayout weights_layout(int B, int Hq, int Hkv, int N, int L) {
   l.nkt = (N + BN - 1) / BN;
   weights_shape(static_cast<long long>(B) * Hkv, l.nqt, l.nkt, true, &l.q_group, &l.splits);
   const long long tile_rows = static_cast<long long>(B) * Hkv * l.nqt * 128;
-  l.lse = al(tile_rows * l.splits * 8);
+  l.lse = al(tile_rows * l.splits * (kWtTiles / l.q_group) * 8);
   l.total = l.lse + al(tile_rows * 4);
   return l;
 }
@@ -1775,10 +1778,11 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
   const long long bg = static_cast<long long>(a.B) * a.Hkv;
   const unsigned sms = static_cast<unsigned>(di->sms);
   p.group = l.q_group;
+  p.parts = l.splits * (kWtTiles / l.q_group);
   p.items = static_cast<int>(bg * ((l.nqt + p.group - 1) / p.group) * l.splits);
   weights_kernel<D, 1><<<std::min<unsigned>(p.items, sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
   const long long rows = bg * l.nqt * 128;
-  if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), 256, 0, st, p))
+  if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>(rows / 32)), 256, 0, st, p))
     return TM_ERR_CUDA;
   int one = 1;
   weights_shape(bg, l.nkt, l.nqt, false, &p.group, &one);

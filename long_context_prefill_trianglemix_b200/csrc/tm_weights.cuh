@@ -15,8 +15,9 @@
 // tensor-core helpers).
 //
 // CTA (576 threads, one per SM, persistent): warps 0-15 are four reduction
-// warpgroups, one per A tile and 128-column S buffer in TMEM; warp 16 loads by
-// TMA; warp 17 issues the MMAs. A warpgroup takes its scores to registers in
+// warpgroups, each with a 128-column S buffer in TMEM; warp 16 loads by TMA; warp
+// 17 issues the MMAs. With four A tiles an item each warpgroup has one; with fewer
+// the warpgroups of a tile take its B tiles in turn (phases). A warpgroup takes its scores to registers in
 // halves, so the next MMA into its buffer runs while it reduces the second half
 // and the other warpgroups work. A q tile packs floor(128 / G) tokens of all G q
 // heads of the group, so short L wastes no rows.
@@ -137,10 +138,11 @@ struct WtParams {
   int tpt;           // tokens of a q tile
   int nqt, nkt;      // q tiles, key tiles (of the longest sequence)
   int splits;        // pass 1: parts of the key range
-  int items, group;  // A tiles of an item: 1, 2 or 4
+  int items, group;  // A tiles of an item: 1, 2 or 4; 4 / group phases
+  int parts;         // splits * phases of pass 1
   float sl2;
   const int* lens;
-  float2* stats;     // pass 1: (m, l) [B Hkv][splits][nqt * 128]
+  float2* stats;     // pass 1: (m, l) [B Hkv][splits * phases of pass 1][nqt * 128]
   float* nlse;       // minus the rows' log-sum-exps [B Hkv][nqt * 128], -inf where there is no row
   float* weights;
   long long stride;
@@ -153,8 +155,9 @@ struct WtCfg {
   static constexpr int kPanel = 128 * 64 * 2;
   static constexpr int kRing = kWtTiles * kTile;
   static constexpr int kLse = kRing + kWtStages * kTile;
-  static constexpr int kBar = kLse + kWtLse * 512;
-  static constexpr int kSmem = kBar + 256 + 1024;
+  static constexpr int kSum = kLse + kWtLse * 512;  // pass 2: later phases' sums, 3 x 128 floats
+  static constexpr int kBar = kSum + 3 * 512;
+  static constexpr int kSmem = kBar + 384 + 1024;
 };
 
 struct WtBars {
@@ -162,6 +165,7 @@ struct WtBars {
   uint64_t b_full[kWtStages], b_empty[kWtStages];
   uint64_t s_full[kWtTiles], s_empty[kWtTiles];
   uint64_t l_full[kWtLse], l_empty[kWtLse];
+  uint64_t x_full[2], x_empty[2];  // [A tile]: the sums above
   uint64_t mma_done;
   uint32_t tmem;
   int abort_flag;
@@ -249,6 +253,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       mbar_init(&bars->l_full[i], 1);
       mbar_init(&bars->l_empty[i], 4 * kWtTiles);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->x_full[i], 4 * (kWtTiles / p.group > 1 ? kWtTiles / p.group - 1 : 1));
+      mbar_init(&bars->x_empty[i], 4);
+    }
     mbar_init(&bars->mma_done, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -332,39 +340,38 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
   } else if (warp == 4 * kWtTiles + 1) {
     const bool leader = elect_one();
-    uint32_t ac[kWtTiles] = {}, sc[kWtTiles] = {}, bc = 0;
+    uint32_t a_par = 0, s_par = 0, bc = 0;  // phase bits of the A tiles and S buffers
+    const int phases = kWtTiles / p.group;
     bool ok = true;
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
       WtItem it;
       if (!wt_item<PASS>(p, i, it) || it.t0 >= it.t1) continue;
       for (int t = it.t0; t < it.t1 && ok; ++t) {
+        const int w0 = ((t - it.t0) & (phases - 1)) * p.group;  // first warpgroup of the phase
         const int st = bc % kWtStages;
         ok = __all_sync(0xffffffffu,
                         wait_bar(&bars->b_full[st], (bc / kWtStages) & 1, abort_flag, kSiteWeights));
-#pragma unroll
-        for (int w = 0; w < kWtTiles; ++w) {
-          if (w >= it.na || !ok) continue;
-          bool here = t > it.t0 || wait_bar(&bars->a_full[w], ac[w] & 1, abort_flag, kSiteWeights);
-          here = here && wait_bar(&bars->s_empty[w], (sc[w] & 1) ^ 1, abort_flag, kSiteWeights);
-          if (!(ok = __all_sync(0xffffffffu, here))) continue;
+        for (int ai = 0; ai < it.na && ok; ++ai) {
+          const int w = w0 + ai;
+          bool here = t > it.t0 || wait_bar(&bars->a_full[ai], (a_par >> ai) & 1, abort_flag, kSiteWeights);
+          here = here && wait_bar(&bars->s_empty[w], ((s_par >> w) & 1) ^ 1, abort_flag, kSiteWeights);
+          if (!(ok = __all_sync(0xffffffffu, here))) break;
           tc_fence_after();
           if (leader) {
-            issue_qk<D>(tmem + w * 128, desc_lo_sw128(sA + w * C::kTile, 16),
+            issue_qk<D>(tmem + w * 128, desc_lo_sw128(sA + ai * C::kTile, 16),
                         desc_lo_sw128(sB + st * C::kTile, 16));
             mma_commit(&bars->s_full[w]);
-            if (t + 1 == it.t1) mma_commit(&bars->a_empty[w]);
+            if (t + 1 == it.t1) mma_commit(&bars->a_empty[ai]);
           }
           __syncwarp();
-          ++sc[w];
+          s_par ^= 1u << w;
         }
         if (!ok) break;
         if (leader) mma_commit(&bars->b_empty[st]);
         __syncwarp();
         ++bc;
       }
-#pragma unroll
-      for (int w = 0; w < kWtTiles; ++w)
-        if (w < it.na) ++ac[w];
+      a_par ^= (1u << it.na) - 1u;
     }
     if (leader) mma_commit(&bars->mma_done);
     __syncwarp();
@@ -374,22 +381,26 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const Quintic kq = quintic();
     const F2 sl2 = both(p.sl2);
-    uint32_t bc = 0, sc = 0;  // B tiles of the CTA, scores of this warpgroup
+    uint32_t bc = 0, sc = 0, xc = 0;  // B tiles of the CTA, scores and items of this warpgroup
+    const int phases = kWtTiles / p.group, ai = wg & (p.group - 1), phase = wg / p.group;
     bool ok = true;
+    // another's B tile: only let its lse slot go
+    auto pass_over = [&](uint32_t n) {
+      const int ls = n % kWtLse;
+      const bool here = __all_sync(
+          0xffffffffu, wait_bar(&bars->l_full[ls], (n / kWtLse) & 1, abort_flag, kSiteWeights));
+      if (here && lane == 0) mbar_arrive(&bars->l_empty[ls]);
+      return here;
+    };
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
       WtItem it;
       if (!wt_item<PASS>(p, i, it)) continue;
-      if (wg >= it.na) {  // no tile for this warpgroup: it only lets the lse slots go
-        for (int t = it.t0; PASS == 2 && t < it.t1 && ok; ++t, ++bc) {
-          const int ls = bc % kWtLse;
-          ok = __all_sync(0xffffffffu, wait_bar(&bars->l_full[ls], (bc / kWtLse) & 1, abort_flag,
-                                                kSiteWeights));
-          if (ok && lane == 0) mbar_arrive(&bars->l_empty[ls]);
-        }
+      if (ai >= it.na) {  // no A tile for this warpgroup
+        for (int t = it.t0; PASS == 2 && t < it.t1 && ok; ++t, ++bc) ok = pass_over(bc);
         continue;
       }
       const int rows = it.len - it.r0;
-      const int a = it.a0 + wg;
+      const int a = it.a0 + ai;
       // pass 1: this thread's row; pass 2: its key
       const int tok = PASS == 1 ? a * p.tpt + r / p.G : 0;
       const bool live = PASS == 1 ? (r < p.tpt * p.G && tok < rows) : a * BN + r < it.len;
@@ -397,12 +408,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int pos = PASS == 1 ? it.r0 + tok : a * BN + r;
       const uint32_t ts = tmem + lane_addr + wg * 128;
       float m = -1.7e38f, sum = 0.f;
-      for (int t = it.t0; t < it.t1; ++t, ++bc, ++sc) {
+      for (int t = it.t0; t < it.t1; ++t, ++bc) {
+        if (((t - it.t0) & (phases - 1)) != phase) {
+          if (PASS == 2 && !(ok = pass_over(bc))) break;
+          continue;
+        }
         const int ls = bc % kWtLse;
         bool here = wait_bar(&bars->s_full[wg], sc & 1, abort_flag, kSiteWeights);
         if (PASS == 2)
           here = here && wait_bar(&bars->l_full[ls], (bc / kWtLse) & 1, abort_flag, kSiteWeights);
         if (!(ok = __all_sync(0xffffffffu, here))) break;
+        ++sc;
         tc_fence_after();
         // columns [c_lo, c_hi) count for this thread
         int c_lo = 0, c_hi = 128;
@@ -498,9 +514,29 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       if (!ok) break;
       const size_t bg = static_cast<size_t>(it.b) * p.Hkv + it.g;
       if (PASS == 1) {
-        p.stats[(bg * p.splits + it.split) * p.nqt * 128 + a * 128 + r] =
-              live ? make_float2(m, sum) : make_float2(0.f, 0.f);
-      } else if (live) {
+        p.stats[(bg * p.parts + it.split * phases + phase) * p.nqt * 128 + a * 128 + r] =
+            live ? make_float2(m, sum) : make_float2(0.f, 0.f);
+        continue;
+      }
+      if (phases > 1) {  // the first phase adds the others' sums, in order
+        float* xs = reinterpret_cast<float*>(smem + C::kSum);
+        if (phase > 0) {
+          ok = __all_sync(0xffffffffu,
+                          wait_bar(&bars->x_empty[ai], (xc & 1) ^ 1, abort_flag, kSiteWeights));
+          if (!ok) break;
+          xs[((phase - 1) * p.group + ai) * 128 + r] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->x_full[ai]);
+        } else {
+          ok = __all_sync(0xffffffffu, wait_bar(&bars->x_full[ai], xc & 1, abort_flag, kSiteWeights));
+          if (!ok) break;
+          for (int k = 0; k + 1 < phases; ++k) sum += xs[(k * p.group + ai) * 128 + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->x_empty[ai]);
+        }
+        ++xc;
+      }
+      if (live && phase == 0) {
         float* dst = p.weights + bg * p.stride + pos;
         *dst = p.accumulate ? *dst + sum : sum;
       }
@@ -515,22 +551,39 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 }
 
 // Joins pass 1's parts: -(m + log2(l)) of each row, -inf for a row that is not there.
+// 32 rows a CTA; eight threads a row share its parts and are joined in order.
 __global__ void __launch_bounds__(256) weights_lse_kernel(const WtParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long per = static_cast<long long>(p.nqt) * 128, n = per * p.B * p.Hkv;
-  const long long i = blockIdx.x * 256LL + threadIdx.x;
-  if (i >= n) return;
-  const long long bg = i / per, r = i - bg * per;
+  __shared__ float2 s_part[8][32];
+  const long long per = static_cast<long long>(p.nqt) * 128;
+  const int x = threadIdx.x & 31, j = threadIdx.x >> 5;
+  const long long i = blockIdx.x * 32LL + x, bg = i / per, r = i - bg * per;
+  const float2* s = p.stats + bg * p.parts * per + r;
+  float m = -1.7e38f, l = 0.f;
+  for (int k0 = j; k0 < p.parts; k0 += 32) {
+    float2 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      v[u] = k0 + 8 * u < p.parts ? s[(k0 + 8 * u) * per] : make_float2(-1.7e38f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float mn = fmax3_nan(m, v[u].x, v[u].x);
+      l = l * ex2(m - mn) + v[u].y * ex2(v[u].x - mn);
+      m = mn;
+    }
+  }
+  s_part[j][x] = make_float2(m, l);
+  __syncthreads();
+  if (j) return;
+  for (int k = 1; k < 8; ++k) {
+    const float2 v = s_part[k][x];
+    const float mn = fmax3_nan(m, v.x, v.x);
+    l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
+    m = mn;
+  }
   const int rows = imin(p.L, wt_len(p, static_cast<int>(bg / p.Hkv)));
   const int c = static_cast<int>(r & 127);
-  float nlse = -INFINITY;
-  if (c < p.tpt * p.G && (r >> 7) * p.tpt + c / p.G < rows) {
-    const float2* s = p.stats + bg * p.splits * per + r;
-    float m = -1.7e38f, l = 0.f;
-    for (int k = 0; k < p.splits; ++k) m = fmaxf(m, s[k * per].x);
-    for (int k = 0; k < p.splits; ++k) l += s[k * per].y * ex2(s[k * per].x - m);
-    nlse = -(m + log2f(l));
-  }
-  p.nlse[i] = nlse;
+  const bool there = c < p.tpt * p.G && (r >> 7) * p.tpt + c / p.G < rows;
+  p.nlse[i] = there ? -(m + log2f(l)) : -INFINITY;
 }
