@@ -51,6 +51,7 @@
 #include "tm.h"
 #include "tm_internal.h"
 #include "tm_kv8.cuh"
+#include "tm_launch.cuh"
 #include "tm_exp2_poly5.h"
 #include "tm_sm100.cuh"
 #include "tm_tiles.cuh"
@@ -1321,26 +1322,6 @@ int set_smem_once(std::atomic<bool>& flag, K kernel, int bytes) {
   return TM_OK;
 }
 
-// A launch that may begin before the kernel ahead of it on the stream has ended
-// (it waits for it with griddepcontrol.wait before it touches memory).
-template <class... P, class... A>
-int launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st,
-                 const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return TM_OK;
-  cudaGetLastError();
-  return TM_ERR_CUDA;
-}
-
 int get_encode_fn() {
   if (g_encode) return TM_OK;
   void* fn = nullptr;
@@ -1780,15 +1761,17 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
   p.group = l.q_group;
   p.parts = l.splits * (kWtTiles / l.q_group);
   p.items = static_cast<int>(bg * ((l.nqt + p.group - 1) / p.group) * l.splits);
-  weights_kernel<D, 1><<<std::min<unsigned>(p.items, sms), kWtThreads, C::kSmem, st>>>(tq, tk, p);
+  if (launch_early(weights_kernel<D, 1>, dim3(std::min<unsigned>(p.items, sms)), kWtThreads, C::kSmem,
+                   st, 1, tq, tk, p))
+    return TM_ERR_CUDA;
   const long long rows = bg * l.nqt * 128;
-  if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>(rows / 32)), 256, 0, st, p))
+  if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>(rows / 32)), 256, 0, st, 1, p))
     return TM_ERR_CUDA;
   int one = 1;
   weights_shape(bg, l.nkt, l.nqt, false, &p.group, &one);
   p.items = static_cast<int>(bg * ((l.nkt + p.group - 1) / p.group));
   if (launch_early(weights_kernel<D, 2>, dim3(std::min<unsigned>(p.items, sms)), kWtThreads, C::kSmem,
-                   st, tq, tk, p))
+                   st, 1, tq, tk, p))
     return TM_ERR_CUDA;
   return counted(3);
 }

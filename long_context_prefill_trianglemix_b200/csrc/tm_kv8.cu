@@ -7,6 +7,7 @@
 #include "tm.h"
 #include "tm_internal.h"
 #include "tm_kv8.cuh"
+#include "tm_launch.cuh"
 
 namespace trimix {
 namespace {
@@ -27,14 +28,18 @@ struct AppendParams {
 // rounding, so k and v are read once: 2 bytes read and 1 written an element.
 template <int FMT, int NC>
 __global__ void __launch_bounds__(kCacheThreads) append_kernel(const AppendParams p) {
+  pdl_launch();
+  pdl_wait();
   const Kv8AppendArgs& a = p.a;
   const int P = a.c.page, D = a.c.D, H = a.c.Hkv, b = blockIdx.z;
-  const int h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+  // heads vary fastest: the CTAs that run together read whole rows of k and v
+  const int frame = blockIdx.x / (2 * H), hv = blockIdx.x - frame * 2 * H;
+  const bool is_v = hv >= H;
+  const int h = is_v ? hv - H : hv;
   const long long cap = static_cast<long long>(a.max_pages) * P;
   const long long len = min(max(static_cast<long long>(a.lens[b]), 0LL), cap);
   const int count = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
-  const int blk = static_cast<int>(len / P) + blockIdx.x;
+  const int blk = static_cast<int>(len / P) + frame;
   if (blk >= a.max_pages) return;
   const long long base = static_cast<long long>(blk) * P;
   const int r_lo = static_cast<int>(max(len - base, 0LL));
@@ -117,6 +122,8 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const AppendParam
 // its step; no token's values are scanned for a maximum.
 template <int FMT>
 __global__ void __launch_bounds__(kCacheThreads) compact_kernel(const Kv8CompactArgs a) {
+  pdl_launch();
+  pdl_wait();
   const int P = a.c.page, D = a.c.D, H = a.c.Hkv, b = blockIdx.z, blk = blockIdx.x, t = threadIdx.x;
   const int h = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
@@ -184,15 +191,18 @@ int append_fmt(const Kv8AppendArgs& a) {
   AppendParams p;
   p.a = a;
   p.row_chunks_log = a.c.D == 128 ? 4 : 3;
-  const dim3 grid((a.n + a.c.page - 2) / a.c.page + 1, 2 * a.c.Hkv, a.B);
+  const long long frames = (a.n + a.c.page - 2LL) / a.c.page + 1;
+  const dim3 grid(static_cast<unsigned>(frames * 2 * a.c.Hkv), 1, a.B);
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+  auto kernel = append_kernel<FMT, 16>;
   switch (a.c.page * a.c.D / (8 * kCacheThreads)) {
-    case 1: append_kernel<FMT, 1><<<grid, kCacheThreads, 0, st>>>(p); break;
-    case 2: append_kernel<FMT, 2><<<grid, kCacheThreads, 0, st>>>(p); break;
-    case 4: append_kernel<FMT, 4><<<grid, kCacheThreads, 0, st>>>(p); break;
-    case 8: append_kernel<FMT, 8><<<grid, kCacheThreads, 0, st>>>(p); break;
-    default: append_kernel<FMT, 16><<<grid, kCacheThreads, 0, st>>>(p); break;
+    case 1: kernel = append_kernel<FMT, 1>; break;
+    case 2: kernel = append_kernel<FMT, 2>; break;
+    case 4: kernel = append_kernel<FMT, 4>; break;
+    case 8: kernel = append_kernel<FMT, 8>; break;
+    default: break;
   }
+  if (launch_early(kernel, grid, kCacheThreads, 0, st, 1, p)) return TM_ERR_CUDA;
   return count_launches(1);
 }
 
@@ -209,10 +219,8 @@ int launch_kv8_compact(const Kv8CompactArgs& a) {
   if (int rc = device_sms(&sms)) return rc;
   const dim3 grid((a.keep + a.c.page - 1) / a.c.page, 2 * a.c.Hkv, a.B);
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-  if (a.c.format == TM_KV_INT8)
-    compact_kernel<TM_KV_INT8><<<grid, kCacheThreads, 0, st>>>(a);
-  else
-    compact_kernel<TM_KV_E4M3><<<grid, kCacheThreads, 0, st>>>(a);
+  auto kernel = a.c.format == TM_KV_INT8 ? compact_kernel<TM_KV_INT8> : compact_kernel<TM_KV_E4M3>;
+  if (launch_early(kernel, grid, kCacheThreads, 0, st, 1, a)) return TM_ERR_CUDA;
   return count_launches(1);
 }
 

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   const Kv8AttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar) + warp * S;
-  asm volatile("griddepcontrol.launch_dependents;");  // the join may take its place early
+  pdl_launch();
   if (tid < 2 * kAttnWarps) s_item[tid] = -1;
   if (tid == 0) {
     *abort_flag = 0;
@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   if (lane == 0)
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
   if (lane == 0) fence_barrier_init();
+  pdl_wait();
   const int longest = unit_prefix(p, pre);
   const long long T = pre[a.B];
   const int parts = parts_of(T, p.grid), cta = blockIdx.x;
@@ -701,8 +702,8 @@ template <int D, int NT>
 __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
   constexpr int V = D / 4, GR = 128 / V;  // float4 lanes of a row, groups of partials
   const int c = blockIdx.y, t = threadIdx.x, lane4 = t % V, grp = t / V;
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
   const int4 rec = p.close[blockIdx.x];
   if (rec.x < 0) return;
   const int item = rec.x, c0 = rec.y, first = rec.z, c1 = rec.w;
@@ -769,9 +770,10 @@ __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
 // The weight of each key: sum over the kv head's rows of 2^(s - lse).
 template <int NT>
 __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
+  pdl_launch();
+  pdl_wait();
   const int bh = blockIdx.y, b = bh / p.a.c.Hkv, h = bh - b * p.a.c.Hkv;
   const long long len = min(static_cast<long long>(clamp_len(p, b)), p.a.weights_stride);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (long long j = blockIdx.x * 256LL + threadIdx.x; j < len; j += gridDim.x * 256LL) {
     float w = 0.f;
     for (int rt = 0; rt < p.RT; ++rt) {
@@ -845,13 +847,15 @@ int attn_run(AttnP& p, DeviceInfo* di) {
   const long long units = static_cast<long long>(a.B) * p.items_per_b * ((p.cap + kUnit - 1) / kUnit);
   p.grid = static_cast<int>(std::min<long long>(std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1),
                                                 (units + kAttnWarps - 1) / kAttnWarps));
-  attn_kernel8<D, FMT, NT><<<p.grid, kAttnThreads, C::kSmem + a.B * 4, st>>>(tk, tv, p);
+  if (launch_early(attn_kernel8<D, FMT, NT>, dim3(p.grid), kAttnThreads, C::kSmem + a.B * 4, st, 1, tk,
+                   tv, p))
+    return TM_ERR_CUDA;
   const dim3 grid(p.grid, 8 * NT);
-  if (launch_early(combine_kernel<D, NT>, grid, 128, 0, st, p)) return TM_ERR_CUDA;
+  if (launch_early(combine_kernel<D, NT>, grid, 128, 0, st, 1, p)) return TM_ERR_CUDA;
   if (!p.scores) return counted(2);
   const long long want = (p.cap + 1023) / 1024;
   const dim3 wgrid(static_cast<unsigned>(want < 256 ? want : 256), a.B * a.c.Hkv);
-  if (launch_early(weight_kernel<NT>, wgrid, 256, 0, st, p)) return TM_ERR_CUDA;
+  if (launch_early(weight_kernel<NT>, wgrid, 256, 0, st, 1, p)) return TM_ERR_CUDA;
   return counted(3);
 }
 

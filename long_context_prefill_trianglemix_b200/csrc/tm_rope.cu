@@ -15,6 +15,7 @@
 
 #include "tm.h"
 #include "tm_internal.h"
+#include "tm_launch.cuh"
 
 namespace trimix {
 namespace {
@@ -83,6 +84,8 @@ __device__ __forceinline__ void turn16(uint4& u, uint4& v, const float (&c)[8], 
 // work is shared by up to Hq + Hkv heads. D / 16 neighbouring threads cover a
 // head's row: 128-byte runs of loads and stores. rot is a multiple of 16.
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+  pdl_launch();
+  pdl_wait();
   const int per = p.D >> 4;
   const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long row = gid / per;
@@ -123,6 +126,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
 
 // Any even rot: one thread per (token, pair or two copied columns, slice of heads).
 __global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p) {
+  pdl_launch();
+  pdl_wait();
   const int per = p.D >> 1;
   const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long row = gid / per;
@@ -183,10 +188,9 @@ int launch_rope(const RopeArgs& a) {
   p.heads_per_slice = static_cast<int>((heads + slices - 1) / slices);
   const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>((heads + p.heads_per_slice - 1) / p.heads_per_slice));
-  if (wide)
-    rope_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(a.stream)>>>(p);
-  else
-    rope_any_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(a.stream)>>>(p);
+  if (launch_early(wide ? rope_kernel : rope_any_kernel, grid, 256, 0,
+                   static_cast<cudaStream_t>(a.stream), 1, p))
+    return TM_ERR_CUDA;
   return count_launches(1);
 }
 

@@ -21,6 +21,7 @@
 
 #include "tm.h"
 #include "tm_internal.h"
+#include "tm_launch.cuh"
 
 namespace trimix {
 namespace {
@@ -66,6 +67,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectAr
   for (int i = t; i < 3 * kBins / 4; i += kSelThreads)
     reinterpret_cast<int4*>(&hist[0][0])[i] = make_int4(0, 0, 0, 0);
   if (t < 2) s_count[t] = 0;
+  pdl_launch();
+  pdl_wait();
   const int n = min(max(a.lens ? a.lens[b] : a.n, 0), a.n);
   int* out = a.index + static_cast<long long>(row) * a.keep;
   const int kept = min(n, a.keep);
@@ -248,26 +251,14 @@ int launch_kv_select(const KvSelectArgs& a) {
   int C = 1;
   const long long rows = static_cast<long long>(a.B) * a.H;
   while (C < kSelMaxCluster && a.n > 4096LL * C && rows * C * 2 <= sms) C *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = static_cast<cudaStream_t>(a.stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = C;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   const int per = (a.n + C - 1) / C;
   auto kernel = per <= 2 * kSelThreads   ? select_kernel<2>
                 : per <= 4 * kSelThreads ? select_kernel<4>
                 : per <= 8 * kSelThreads ? select_kernel<8>
                                          : select_kernel<kSelMaxKeys>;
-  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
-    cudaGetLastError();
+  if (launch_early(kernel, dim3(static_cast<unsigned>(rows * C)), kSelThreads, 0,
+                   static_cast<cudaStream_t>(a.stream), C, a))
     return TM_ERR_CUDA;
-  }
   return count_launches(1);
 }
 

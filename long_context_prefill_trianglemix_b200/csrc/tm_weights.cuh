@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // pass 2: the lse kernel's results
+  pdl_launch();
+  pdl_wait();
   const uint32_t tmem = bars->tmem;
   const uint32_t sA = smem_addr(smem), sB = sA + C::kRing;
   const int q_bytes = q_rows * D * 2;
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 // Joins pass 1's parts: -(m + log2(l)) of each row, -inf for a row that is not there.
 // 32 rows a CTA; eight threads a row share its parts and are joined in order.
 __global__ void __launch_bounds__(256) weights_lse_kernel(const WtParams p) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
   __shared__ float2 s_part[8][32];
   const long long per = static_cast<long long>(p.nqt) * 128;
   const int x = threadIdx.x & 31, j = threadIdx.x >> 5;
