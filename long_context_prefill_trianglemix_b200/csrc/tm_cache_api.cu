@@ -200,7 +200,6 @@ TM_API int tm_kv8_append(const void* k, const void* v, long long k_stride, long 
   const long long w = static_cast<long long>(Hkv) * D;
   if (bad_stride(k_stride, w) || bad_stride(v_stride, w)) return TM_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * n_src > kIntMax) return TM_ERR_INVALID_ARG;
-  if ((static_cast<long long>(n) / page + 2) * 2 * Hkv > kIntMax) return TM_ERR_INVALID_ARG;
   const long long pool = static_cast<long long>(num_pages) * w * page;
   const long long kb = ((static_cast<long long>(B) * n_src - 1) * k_stride + w) * 2;
   const long long vb = ((static_cast<long long>(B) * n_src - 1) * v_stride + w) * 2;

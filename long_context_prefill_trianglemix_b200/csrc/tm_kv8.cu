@@ -18,102 +18,141 @@ constexpr int kCacheThreads = 128;
 
 struct AppendParams {
   Kv8AppendArgs a;
-  int row_chunks_log;  // log2 of the 8-element chunks of a row
+  long long frames;  // blocks a sequence's new tokens can touch
 };
 
-// One CTA per (touched block, head, k or v). The block's range becomes the
-// larger of its old range (if it already holds tokens of this sequence) and the
-// new tokens' largest |x|; where it grows, the old codes are moved to it.
-// The block's new elements stay in registers between the maximum and the
-// rounding, so k and v are read once: 2 bytes read and 1 written an element.
-template <int FMT, int NC>
-__global__ void __launch_bounds__(kCacheThreads) append_kernel(const AppendParams p) {
+// A block's range becomes the larger of its old range (if it already holds tokens
+// of this sequence) and the new tokens' largest |x|; where it grows, the old codes
+// are moved to it. BW warps share a block of P = 32 BW NC 8 / D rows, NC chunks of 8
+// elements a lane, and a CTA takes several small blocks; the elements stay in
+// registers between the maximum and the rounding, so k and v are read once: 2 bytes
+// read and 1 written an element. Heads vary fastest over the grid: CTAs that run
+// together read whole rows. A block that is new throughout (all but the first and
+// last of a prompt) takes the path without bounds: 17 instructions an element with
+// them kept this kernel at 0.7 of the memory's rate.
+template <int FMT, int D, int BW, int NC>
+__global__ void __launch_bounds__(BW > 4 ? BW * 32 : 128) append_kernel(const AppendParams p) {
+  constexpr int P = 32 * BW * NC * 8 / D, NT = 32 * BW, RC = D / 8, STEP = NT / RC;
   pdl_launch();
   pdl_wait();
+  __shared__ uint32_t red[8];
   const Kv8AppendArgs& a = p.a;
-  const int P = a.c.page, D = a.c.D, H = a.c.Hkv, b = blockIdx.z;
-  // heads vary fastest: the CTAs that run together read whole rows of k and v
-  const int frame = blockIdx.x / (2 * H), hv = blockIdx.x - frame * 2 * H;
-  const bool is_v = hv >= H;
-  const int h = is_v ? hv - H : hv;
+  const int H = a.c.Hkv, b = blockIdx.z;
+  const bool is_v = blockIdx.x >= static_cast<unsigned>(H);
+  const int h = is_v ? blockIdx.x - H : blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp / BW, t = (warp % BW) * 32 + lane;  // block of the trip, thread of the block
+  const int per = (blockDim.x >> 5) / BW;
   const long long cap = static_cast<long long>(a.max_pages) * P;
   const long long len = min(max(static_cast<long long>(a.lens[b]), 0LL), cap);
   const int count = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
-  const int blk = static_cast<int>(len / P) + frame;
-  if (blk >= a.max_pages) return;
-  const long long base = static_cast<long long>(blk) * P;
-  const int r_lo = static_cast<int>(max(len - base, 0LL));
-  const int r_hi = static_cast<int>(min(len + count - base, static_cast<long long>(P)));
-  if (r_hi <= r_lo) return;
-  const int page = a.table[static_cast<long long>(b) * a.max_pages + blk];
-  if (page < 0 || page >= a.c.num_pages) return;
-
-  const int t = threadIdx.x, cl = p.row_chunks_log, cm = (1 << cl) - 1;
+  const long long first = len / P;
   const long long stride = is_v ? a.v_stride : a.k_stride;
   const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v : a.k) +
-                        static_cast<long long>(b) * a.n_src * stride + h * D;
-  const long long tok0 = base - len;  // source token of the block's row 0
+                        static_cast<long long>(b) * a.n_src * stride + h * D + (t % RC) * 8;
   const int* index = a.index ? a.index + (static_cast<long long>(b) * H + h) * a.n : nullptr;
-  uint4 x[NC];
-  uint32_t mx = 0;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int ch = i * kCacheThreads + t, row = ch >> cl;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (row >= r_lo && row < r_hi) {
-      long long tok = tok0 + row;
-      if (index) tok = index[tok];
-      if (tok >= 0 && tok < a.n_src)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(src + tok * stride) + (ch & cm));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {  // |x| of bf16 orders as its bits do, NaN above infinity
-    const uint32_t m01 = __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
-    const uint32_t m23 = __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
-    mx = __vmaxu2(mx, __vmaxu2(m01, m23));
-  }
-  __shared__ uint32_t red[kCacheThreads / 32];
-  mx = warp_max(max(mx & 0xFFFFu, mx >> 16));
-  if ((t & 31) == 0) red[t >> 5] = mx;
-  float* range = (is_v ? a.c.v_range : a.c.k_range) + static_cast<long long>(page) * H + h;
-  const float r_old = r_lo > 0 ? *range : 0.f;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kCacheThreads / 32; ++w) mx = max(mx, red[w]);
-  const uint32_t r_bits = max(mx << 16, __float_as_uint(r_old));  // NaN and inf propagate
-  const float r = __uint_as_float(r_bits);
 
-  uint8_t* codes = static_cast<uint8_t*>(is_v ? a.c.v8 : a.c.k8) +
-                   (static_cast<long long>(page) * H + h) * P * D;
-  const bool live = finite(r) && r > 0.f;
-  // A range below 2^-64 would overflow F / r: both sides are scaled by 2^64.
-  const float up = r < 5.421010862427522e-20f ? 18446744073709551616.f : 1.f;
-  const float inv = live ? __fdiv_rn(full<FMT>(), r * up) : 0.f;
+  for (long long f0 = static_cast<long long>(blockIdx.y) * per; f0 < p.frames;
+       f0 += static_cast<long long>(gridDim.y) * per) {  // the same trips for the whole CTA
+    const long long blk = first + f0 + sub;
+    const long long base = blk * P;
+    // rows [r_lo, r_hi) of the block are new; none if the block is not touched or not there
+    const int r_lo = static_cast<int>(max(len - base, 0LL));
+    int r_hi = static_cast<int>(min(len + count - base, static_cast<long long>(P)));
+    int page = -1;
+    if (f0 + sub < p.frames && blk < a.max_pages && r_hi > r_lo)
+      page = a.table[static_cast<long long>(b) * a.max_pages + blk];
+    if (page < 0 || page >= a.c.num_pages) r_hi = r_lo;
+    const bool used = r_hi > r_lo;
+
+    const long long tok0 = base - len;  // source token of the block's row 0
+    const bool full = !index && r_lo == 0 && r_hi == P;  // then n <= n_src bounds the tokens
+    uint4 x[NC];
+    if (full) {
+      const uint16_t* at = src + (tok0 + t / RC) * stride;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int ch = i * kCacheThreads + t, row = ch >> cl;
-    if (row < r_lo || row >= r_hi) continue;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    float f[8];
+      for (int i = 0; i < NC; ++i) {
+        x[i] = __ldg(reinterpret_cast<const uint4*>(at));
+        at += STEP * stride;
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(w[e] << 16) * up * inv;
-      f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * up * inv;
+      for (int i = 0; i < NC; ++i) {
+        const int row = t / RC + i * STEP;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (row >= r_lo && row < r_hi) {
+          long long tok = tok0 + row;
+          if (index) tok = index[tok];
+          if (tok >= 0 && tok < a.n_src)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(src + tok * stride));
+        }
+      }
     }
-    uint2 o = make_uint2(encode4<FMT>(f[0], f[1], f[2], f[3]), encode4<FMT>(f[4], f[5], f[6], f[7]));
-    if (!live) o = make_uint2(0, 0);
-    reinterpret_cast<uint2*>(codes)[ch] = o;
-  }
-  if (r_lo > 0 && r != r_old) {
-    const float ratio = live ? __fdiv_rn(r_old, r) : 0.f;
-    for (int ch = t; ch < (r_lo << cl); ch += kCacheThreads) {
-      uint2 o = reinterpret_cast<uint2*>(codes)[ch];
-      o = live ? make_uint2(rescale4<FMT>(o.x, ratio), rescale4<FMT>(o.y, ratio)) : make_uint2(0, 0);
-      reinterpret_cast<uint2*>(codes)[ch] = o;
+    float* range = (is_v ? a.c.v_range : a.c.k_range) + static_cast<long long>(page) * H + h;
+    const float r_old = used && r_lo > 0 ? *range : 0.f;
+    __nv_bfloat162 top = __halves2bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
     }
+    uint32_t mx = *reinterpret_cast<const uint32_t*>(&top);  // bits of |x| order as the values, NaN on top
+    mx = warp_max(max(mx & 0xFFFFu, mx >> 16));
+    if (BW > 1) {
+      if (lane == 0) red[warp] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < BW; ++w) mx = max(mx, red[sub * BW + w]);
+      __syncthreads();  // read before the next trip writes it, and *range before it is replaced
+    }
+    __syncwarp();
+    if (!used) continue;
+    const uint32_t r_bits = max(mx << 16, __float_as_uint(r_old));  // NaN and inf propagate
+    const float r = __uint_as_float(r_bits);
+
+    uint2* codes = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.c.v8 : a.c.k8) +
+                                            (static_cast<long long>(page) * H + h) * (P * D)) + t;
+    const bool live = finite(r) && r > 0.f;
+    // A range below 2^-64 would overflow F / r: both sides are scaled by 2^64.
+    const bool tiny = r < 5.421010862427522e-20f;
+    const float inv = live ? code_factor<FMT>(tiny ? r * 18446744073709551616.f : r) : 0.f;
+    if (full && live && !tiny) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) codes[i * NT] = encode8<FMT, false>(x[i], inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int row = t / RC + i * STEP;
+        if (row < r_lo || row >= r_hi) continue;
+        uint2 o = tiny ? encode8<FMT, true>(x[i], inv) : encode8<FMT, false>(x[i], inv);
+        codes[i * NT] = live ? o : make_uint2(0, 0);
+      }
+    }
+    if (r_lo > 0 && r != r_old) {
+      const float ratio = live ? __fdiv_rn(r_old, r) : 0.f;
+      for (int ch = t; ch < r_lo * RC; ch += NT) {
+        const uint2 o = codes[ch - t];
+        codes[ch - t] =
+            live ? make_uint2(rescale4<FMT>(o.x, ratio), rescale4<FMT>(o.y, ratio)) : make_uint2(0, 0);
+      }
+    }
+    if (t == 0) *range = r;
   }
-  if (t == 0) *range = r;
+}
+
+template <int FMT, int D, int BW, int NC>
+int append_run(AppendParams& p) {
+  const Kv8AppendArgs& a = p.a;
+  // a short call leaves a block to a CTA of its own, a long one fills CTAs of four warps
+  const int threads = p.frames < 8 || BW > 4 ? 32 * BW : 128;
+  const long long per = threads / (32 * BW), groups = (p.frames + per - 1) / per;
+  const dim3 grid(2 * a.c.Hkv, static_cast<unsigned>(groups < 65535 ? groups : 65535), a.B);
+  if (launch_early(append_kernel<FMT, D, BW, NC>, grid, threads, 0, static_cast<cudaStream_t>(a.stream),
+                   1, p))
+    return TM_ERR_CUDA;
+  return count_launches(1);
 }
 
 // One CTA per (new block, head, k or v): gathers the block's tokens from the old
@@ -190,20 +229,21 @@ template <int FMT>
 int append_fmt(const Kv8AppendArgs& a) {
   AppendParams p;
   p.a = a;
-  p.row_chunks_log = a.c.D == 128 ? 4 : 3;
-  const long long frames = (a.n + a.c.page - 2LL) / a.c.page + 1;
-  const dim3 grid(static_cast<unsigned>(frames * 2 * a.c.Hkv), 1, a.B);
-  cudaStream_t st = static_cast<cudaStream_t>(a.stream);
-  auto kernel = append_kernel<FMT, 16>;
-  switch (a.c.page * a.c.D / (8 * kCacheThreads)) {
-    case 1: kernel = append_kernel<FMT, 1>; break;
-    case 2: kernel = append_kernel<FMT, 2>; break;
-    case 4: kernel = append_kernel<FMT, 4>; break;
-    case 8: kernel = append_kernel<FMT, 8>; break;
-    default: break;
+  p.frames = (a.n + a.c.page - 2LL) / a.c.page + 1;
+  if (a.c.D == 128) {
+    switch (a.c.page) {
+      case 16: return append_run<FMT, 128, 1, 8>(p);
+      case 32: return append_run<FMT, 128, 2, 8>(p);
+      case 64: return append_run<FMT, 128, 4, 8>(p);
+      default: return append_run<FMT, 128, 8, 8>(p);
+    }
   }
-  if (launch_early(kernel, grid, kCacheThreads, 0, st, 1, p)) return TM_ERR_CUDA;
-  return count_launches(1);
+  switch (a.c.page) {
+    case 16: return append_run<FMT, 64, 1, 4>(p);
+    case 32: return append_run<FMT, 64, 1, 8>(p);
+    case 64: return append_run<FMT, 64, 2, 8>(p);
+    default: return append_run<FMT, 64, 4, 8>(p);
+  }
 }
 
 }  // namespace

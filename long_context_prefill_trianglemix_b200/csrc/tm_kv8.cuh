@@ -9,6 +9,9 @@
 //     it or at least 2^-16 (int8) or 2^-13 (e4m3) away, relative to it, while
 //     x * fl(F / r) is within 2^-22. Dropping the product's last bits (snap)
 //     therefore puts every tie back on its border and moves nothing across one.
+//   - For int8 the only such ties are x = r / 2 (63.5, to the even 64) and those of
+//     r = 254 * 2^e, where F / r is exact: rounding F / r upwards settles both, and
+//     one FMA with 1.5 * 2^23 multiplies and rounds.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,6 +21,7 @@
 #include <cstdint>
 
 #include "tm.h"
+#include "tm_sm100.cuh"
 
 namespace trimix {
 namespace kv8 {
@@ -70,6 +74,42 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&f)[4]) {
     f[0] = __low2float(l); f[1] = __high2float(l);
     f[2] = __low2float(h); f[3] = __high2float(h);
   }
+}
+
+// F / r for encode8, r of 8 significant bits.
+template <int FMT>
+__device__ __forceinline__ float code_factor(float r) {
+  return FMT == TM_KV_INT8 ? __fdiv_ru(full<FMT>(), r) : __fdiv_rn(full<FMT>(), r);
+}
+
+// The codes of 8 bf16 values: x[e] * f to the nearest code, two values an instruction.
+// e4m3 snaps the product to 17 bits by Veltkamp's splitting (hi = g + (y - g), g = 129 y).
+// TINY: x is scaled by 2^64 first (f is that of the range scaled alike).
+template <int FMT, bool TINY>
+__device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
+  using namespace sm100;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const F2 ff = pack2(f, f);
+  uint32_t c[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    F2 v = pack2(w[e] << 16, w[e] & 0xFFFF0000u);
+    if (TINY) v = mul2(v, pack2(18446744073709551616.f, 18446744073709551616.f));
+    float a, b;
+    if (FMT == TM_KV_INT8) {
+      unpack2(fma2(v, ff, pack2(12582912.f, 12582912.f)), a, b);
+      c[2 * e] = __float_as_uint(a);
+      c[2 * e + 1] = __float_as_uint(b);
+    } else {
+      const F2 y = mul2(v, ff);
+      const F2 g = mul2(y, pack2(129.f, 129.f));
+      unpack2(add2(g, fma2(g, pack2(-1.f, -1.f), y)), a, b);
+      c[e] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+  if (FMT == TM_KV_INT8)
+    return make_uint2(pack_bytes(c[0], c[1], c[2], c[3]), pack_bytes(c[4], c[5], c[6], c[7]));
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // Codes of a block of range r0 in the same block at range r >= r0: rne(c r0 / r),
