@@ -226,7 +226,8 @@ TM_API int tm_kv8_compact(const int* index, int keep, const int* kept, const int
   if (int rc = validate_cache(k8, v8, k_range, v_range, num_pages, page, format, Hkv, D)) return rc;
   if (int rc = validate_table(table, B, max_pages, page)) return rc;
   if (int rc = validate_table(new_table, B, new_max_pages, page)) return rc;
-  if (static_cast<long long>(new_max_pages) * page < keep) return TM_ERR_INVALID_ARG;
+  if (static_cast<long long>(new_max_pages) * page < keep || (keep - 1) / page >= 65535)
+    return TM_ERR_INVALID_ARG;
   if ((weights != nullptr) != (new_weights != nullptr)) return TM_ERR_INVALID_ARG;
   if (!aligned(index, 4) || !aligned(kept, 4) || !aligned(lens, 4) || !aligned(weights, 4) ||
       !aligned(new_weights, 4))

@@ -29,51 +29,18 @@ namespace kv8 {
 template <int FMT>
 __device__ constexpr float full() { return FMT == TM_KV_INT8 ? 127.f : 448.f; }
 
-// y with its significand rounded to 24 - BITS bits.
-template <int BITS>
-__device__ __forceinline__ float snap(float y) {
-  const uint32_t u = __float_as_uint(y);
-  return __uint_as_float((u + (1u << (BITS - 1))) & ~((1u << BITS) - 1u));
-}
-
-// The int8 code (in the low byte) nearest to y, |y| < 2^22: adding 1.5 * 2^23
-// rounds to an integer, ties to even, and leaves it in the low bits.
-__device__ __forceinline__ uint32_t round_low(float y) {
-  return __float_as_uint(y + 12582912.f);
-}
-
 __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return l | (h << 16);
-}
-
-// Four codes of the quotients y (already within 2^-22 of the real ones).
-template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-  if (FMT == TM_KV_INT8)
-    return pack_bytes(round_low(snap<4>(a)), round_low(snap<4>(b)), round_low(snap<4>(c)),
-                      round_low(snap<4>(d)));
-  return pack_e4m3(snap<7>(a), snap<7>(b), snap<7>(c), snap<7>(d));
-}
-
-// Four codes as floats.
-template <int FMT>
-__device__ __forceinline__ void decode4(uint32_t w, float (&f)[4]) {
-  if (FMT == TM_KV_INT8) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = static_cast<float>(static_cast<int8_t>(w >> (8 * e)));
-  } else {
-    const __half2 l(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3));
-    const __half2 h(
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3));
-    f[0] = __low2float(l); f[1] = __high2float(l);
-    f[2] = __low2float(h); f[3] = __high2float(h);
-  }
+// Both values rounded to 24 - BITS significant bits (Veltkamp's splitting: hi = g + (y - g),
+// g = (2^BITS + 1) y).
+template <int BITS>
+__device__ __forceinline__ sm100::F2 snap2(sm100::F2 y) {
+  using namespace sm100;
+  const float c = static_cast<float>((1 << BITS) + 1);
+  const F2 g = mul2(y, pack2(c, c));
+  return add2(g, fma2(g, pack2(-1.f, -1.f), y));
 }
 
 // F / r for encode8, r of 8 significant bits.
@@ -83,7 +50,6 @@ __device__ __forceinline__ float code_factor(float r) {
 }
 
 // The codes of 8 bf16 values: x[e] * f to the nearest code, two values an instruction.
-// e4m3 snaps the product to 17 bits by Veltkamp's splitting (hi = g + (y - g), g = 129 y).
 // TINY: x is scaled by 2^64 first (f is that of the range scaled alike).
 template <int FMT, bool TINY>
 __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
@@ -101,9 +67,7 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
       c[2 * e] = __float_as_uint(a);
       c[2 * e + 1] = __float_as_uint(b);
     } else {
-      const F2 y = mul2(v, ff);
-      const F2 g = mul2(y, pack2(129.f, 129.f));
-      unpack2(add2(g, fma2(g, pack2(-1.f, -1.f), y)), a, b);
+      unpack2(snap2<7>(mul2(v, ff)), a, b);
       c[e] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     }
   }
@@ -116,9 +80,27 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
 // ratio = r0 / r.
 template <int FMT>
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
-  float f[4];
-  decode4<FMT>(w, f);
-  return encode4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+  using namespace sm100;
+  const F2 rr = pack2(ratio, ratio);
+  float a, b, c, d;
+  if (FMT == TM_KV_INT8) {
+    // 2^23 + code + 128 by its bits, so that one addition gives the code as a float
+    const uint32_t u = w ^ 0x80808080u;
+    const F2 bias = pack2(-8388736.f, -8388736.f), round = pack2(12582912.f, 12582912.f);
+    F2 x = add2(pack2(__byte_perm(u, 0x4B000000u, 0x7440), __byte_perm(u, 0x4B000000u, 0x7441)), bias);
+    F2 y = add2(pack2(__byte_perm(u, 0x4B000000u, 0x7442), __byte_perm(u, 0x4B000000u, 0x7443)), bias);
+    unpack2(add2(snap2<4>(mul2(x, rr)), round), a, b);
+    unpack2(add2(snap2<4>(mul2(y, rr)), round), c, d);
+    return pack_bytes(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+  }
+  const float2 x = __half22float2(
+      __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
+  const float2 y = __half22float2(
+      __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)));
+  unpack2(snap2<7>(mul2(pack2(x.x, x.y), rr)), a, b);
+  unpack2(snap2<7>(mul2(pack2(y.x, y.y), rr)), c, d);
+  return __byte_perm(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3),
+                     __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3), 0x5410);
 }
 
 __device__ __forceinline__ bool finite(float r) {
