@@ -1292,7 +1292,7 @@ struct DeviceInfo {
   std::atomic<bool> probe_attr_set[2] = {false, false};
   std::atomic<bool> disc_attr_set[2] = {false, false};
   std::atomic<bool> weights_attr_set[4] = {false, false, false, false};
-  std::atomic<bool> kv8_attr_set[8] = {};
+  std::atomic<bool> kv8_attr_set[16] = {};
 };
 
 constexpr int kMaxDevices = 64;

@@ -38,13 +38,13 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kAttnThreads = 256;
-constexpr int kAttnWarps = kAttnThreads / 32;
-constexpr int kUnit = 16;       // tokens
+constexpr int kWarps = 8;       // of a CTA
 constexpr int kMaxAttnBatch = 4096;
 constexpr int kMaxSms = 192;    // workspaces are sized for this many
 constexpr float kLift = 8.f;    // log2 of the scale of P against the reference
 constexpr float kSlack = 7.f;   // scores may exceed the reference by this
+constexpr float kFar = 0x1p-10f;  // P takes a V range in while it is this much of the reference
+constexpr float kFarthest = 0x1p-70f;  // (further down it adds nothing that fp32 would hold)
 constexpr float kLowest = -1.7e38f;
 
 struct AttnP {
@@ -67,16 +67,16 @@ __device__ __forceinline__ int clamp_len(const AttnP& p, int b) {
 }
 
 // How the line of T units is cut for `grid` CTAs: at least one unit a warp.
-__device__ __forceinline__ int parts_of(long long T, int grid) {
-  const long long most = (T + kAttnWarps - 1) / kAttnWarps;
+__device__ __forceinline__ int parts_of(long long T, int grid, int warps) {
+  const long long most = (T + warps - 1) / warps;
   return static_cast<int>(most < grid ? (most < 1 ? 1 : most) : grid);
 }
 
 // Where every item is short, at most two warps' shares, none is cut: a boundary that
 // falls inside one moves to its start. (Among long items that would unbalance the
 // warps: 24 sequences of 327 to 32768 tokens took 57 us so, 51 us cut evenly.)
-__device__ __forceinline__ bool whole_items(long long T, int grid, int longest) {
-  return longest * static_cast<long long>(grid) * kAttnWarps <= 2 * T || longest <= 2;
+__device__ __forceinline__ bool whole_items(long long T, int grid, int warps, int longest) {
+  return longest * static_cast<long long>(grid) * warps <= 2 * T || longest <= 2;
 }
 
 __device__ __forceinline__ int sequence_of(const int* pre, int B, int x) {
@@ -134,42 +134,50 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& first, uint32_t& sec
   }
 }
 
-// Shared memory of the kernel: each warp has a ring of S units (K rows, then V
-// rows, 128-byte swizzled by the TMA load).
-template <int D, int NT>
+// UT tiles of 16 tokens make a unit. Two halve what a unit costs besides its codes
+// (under the power cap, where the clock falls to 1.6 GHz, instruction issue and not
+// memory bounds this kernel) but need registers or shared memory that one row tile of
+// D = 128 has a better use for: 16 warps an SM with one tile each took 337 us where 12
+// with two took 350 (8 sequences of 131072 tokens, e4m3). Each warp has a ring of S
+// units (K rows, then V rows, 128-byte swizzled by the TMA load): one unit loads while
+// another is computed; more in flight is slower (three deep 347 us, two deep 324).
+template <int D, int NT, int UT>
 struct AttnCfg {
-  // One unit loads while another is computed. More in flight is slower: 3 deep, 8 sequences
-  // of 131072 tokens took 347 us, 2 deep 324 us.
-  static constexpr int S = D == 64 ? (NT == 1 ? 4 : 3) : 2;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;  // an SM, 128 and 255 registers a thread
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kUnit = 16 * UT;
   static constexpr int kHalf = kUnit * D;  // bytes of a unit's K or V
+  static constexpr int S = kHalf == 1024 ? 4 : 2;
   static constexpr int kWarpRing = S * 2 * kHalf;
-  static constexpr int kMl = kAttnWarps * kWarpRing;  // float2 [2 warps][8 NT]
-  static constexpr int kBar = kMl + 2 * kAttnWarps * 8 * NT * 8;
-  static constexpr int kItem = kBar + kAttnWarps * S * 8;
-  static constexpr int kPre = kItem + 2 * kAttnWarps * 4 + 16;  // int [B + 1]
-  static constexpr int kSmem = kPre + 16 + 1024;                // + 4 B, alignment slack
+  static constexpr int kMl = kWarps * kWarpRing;  // float2 [2 warps][8 NT]
+  static constexpr int kBar = kMl + 2 * kWarps * 8 * NT * 8;
+  static constexpr int kItem = kBar + kWarps * S * 8;
+  static constexpr int kPre = kItem + 2 * kWarps * 4 + 16;  // int [B + 1]
+  static constexpr int kSmem = kPre + 16 + 1024;            // + 4 B, alignment slack
   static_assert(8 * NT * D * 4 <= kWarpRing, "a partial must fit a warp's ring");
 };
 
 // Where one lane's unit of the line lies.
 struct UnitAt {
   int item, u;
-  int row;  // TMA row of the unit, -1 if its page is not there
-  float kr, vr;
+  int row;       // TMA row of the unit, -1 if its page is not there
+  float kr, vr;  // its ranges; kr is kMissing if its page is not there
 };
+constexpr float kMissing = -1.f;  // ranges are >= 0
 
-template <int D>
+template <int D, int UT>
 __device__ __forceinline__ UnitAt locate(const AttnP& p, const int* pre, int x, int xe) {
   UnitAt at;
   at.item = -1; at.u = 0; at.row = -1;
-  at.kr = at.vr = 0.f;
+  at.kr = kMissing;
+  at.vr = 0.f;
   if (x >= xe) return at;
   const int lo = sequence_of(pre, p.a.B, x);
   const int U = (pre[lo + 1] - pre[lo]) / p.items_per_b;
   const int it = (x - pre[lo]) / U;
   at.u = x - pre[lo] - it * U;
   at.item = lo * p.items_per_b + it;
-  const int tok0 = at.u * kUnit;
+  const int tok0 = at.u * 16 * UT;
   const int page = __ldg(p.a.table + static_cast<long long>(lo) * p.a.max_pages + (tok0 >> p.page_log));
   if (static_cast<unsigned>(page) < static_cast<unsigned>(p.a.c.num_pages)) {
     const long long block = static_cast<long long>(page) * p.a.c.Hkv + it / p.RT;
@@ -188,14 +196,15 @@ __device__ __forceinline__ void load_ranges(const AttnP& p, UnitAt& at) {
 
 // Prefix sums of the sequences' units (times items per sequence) in shared memory;
 // returns the units of the longest.
+template <int W, int UT>
 __device__ __forceinline__ int unit_prefix(const AttnP& p, int* pre) {
-  __shared__ int s_warp[kAttnWarps], s_most[kAttnWarps];
+  __shared__ int s_warp[W], s_most[W];
   int most = 0;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   int carry = 0;
-  for (int b0 = 0; b0 < p.a.B; b0 += kAttnThreads) {
+  for (int b0 = 0; b0 < p.a.B; b0 += 32 * W) {
     const int b = b0 + t;
-    const int U = b < p.a.B ? (clamp_len(p, b) + kUnit - 1) / kUnit : 0;
+    const int U = b < p.a.B ? (clamp_len(p, b) + 16 * UT - 1) / (16 * UT) : 0;
     most = max(most, U);
     int x = U * p.items_per_b;
     const int own = x;
@@ -207,7 +216,7 @@ __device__ __forceinline__ int unit_prefix(const AttnP& p, int* pre) {
     if (lane == 31) s_warp[w] = x;
     __syncthreads();
     int before = carry;
-    for (int i = 0; i < kAttnWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
       if (i < w) before += s_warp[i];
       carry += s_warp[i];
     }
@@ -219,7 +228,7 @@ __device__ __forceinline__ int unit_prefix(const AttnP& p, int* pre) {
   if (t == 0) pre[p.a.B] = carry;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kAttnWarps; ++i) most = max(most, s_most[i]);
+  for (int i = 0; i < W; ++i) most = max(most, s_most[i]);
   return most;
 }
 
@@ -234,23 +243,23 @@ __device__ __forceinline__ uint16_t* out_row(const AttnP& p, int b, int h, int r
          ((static_cast<long long>(b) * p.a.nq + i) * p.a.Hq + h * p.G + (r - i * p.G)) * D;
 }
 
-template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
+template <int D, int FMT, int NT, int UT>
+__global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, UT>::kCtas)
     attn_kernel8(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ AttnP p) {
-  using C = AttnCfg<D, NT>;
-  constexpr int S = C::S;
+  using C = AttnCfg<D, NT, UT>;
+  constexpr int S = C::S, W = kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kMl);
   int* s_item = reinterpret_cast<int*>(smem + C::kItem);  // item of the slot's partial, or -1
-  volatile int* abort_flag = s_item + 2 * kAttnWarps;
+  volatile int* abort_flag = s_item + 2 * W;
   int* pre = reinterpret_cast<int*>(smem + C::kPre);
   const Kv8AttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar) + warp * S;
   pdl_launch();
-  if (tid < 2 * kAttnWarps) s_item[tid] = -1;
+  if (tid < 2 * W) s_item[tid] = -1;
   if (tid == 0) {
     *abort_flag = 0;
     tma_prefetch_desc(&tk);
@@ -260,27 +269,26 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
   if (lane == 0) fence_barrier_init();
   pdl_wait();
-  const int longest = unit_prefix(p, pre);
+  const int longest = unit_prefix<W, UT>(p, pre);
   const long long T = pre[a.B];
-  const int parts = parts_of(T, p.grid), cta = blockIdx.x;
+  const int parts = parts_of(T, p.grid, W), cta = blockIdx.x;
   for (int z = cta; z < a.B; z += gridDim.x) {  // sequences without tokens: zeros
     if (pre[z + 1] != pre[z]) continue;
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
                                         static_cast<long long>(z) * a.nq * a.Hq * D);
-    for (int i = tid; i < a.nq * a.Hq * (D / 8); i += kAttnThreads) o[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < a.nq * a.Hq * (D / 8); i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
   }
   if (cta >= parts) {
     if (tid == 0) p.close[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
   // the CTA's part [cs, ce) and this warp's [xs, xe): lanes 0, 1, 2, 3 look up one bound each
-  const bool whole = whole_items(T, p.grid, longest);
+  const bool whole = whole_items(T, p.grid, W, longest);
   int cs, ce, xs, xe;
   {
     const int c0 = static_cast<int>(T * cta / parts), c1 = static_cast<int>(T * (cta + 1) / parts);
     const long long w = warp + (lane & 1);
-    const int x = (lane & 2) ? c0 + static_cast<int>((c1 - c0) * w / kAttnWarps)
-                             : (lane & 1) ? c1 : c0;
+    const int x = (lane & 2) ? c0 + static_cast<int>((c1 - c0) * w / W) : (lane & 1) ? c1 : c0;
     const int at = whole ? item_start(p, pre, x) : x;
     cs = __shfl_sync(0xffffffffu, at, 0);
     ce = __shfl_sync(0xffffffffu, at, 1);
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   const uint32_t ring_addr = smem_addr(ring);
 
   // Lane i & 31 holds where unit i lies; the next 32 are looked up a batch ahead.
-  UnitAt cur = locate<D>(p, pre, xs + lane, xe), nxt = cur;
+  UnitAt cur = locate<D, UT>(p, pre, xs + lane, xe), nxt = cur;
   auto issue = [&](int i, int batch) {
     if (i >= n_units || lane != (i & 31)) return;
     const int row = (i >> 5) == batch ? cur.row : nxt.row;
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   };
   for (int i = 0; i < S - 1; ++i) issue(i, 0);
   load_ranges<D>(p, cur);
-  nxt = locate<D>(p, pre, xs + 32 + lane, xe);
+  nxt = locate<D, UT>(p, pre, xs + 32 + lane, xe);
   load_ranges<D>(p, nxt);
   if (tid == 0) {
     // does the item that holds the part's first unit begin before it and end in it?
@@ -327,8 +335,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     p.close[cta] = rec;
   }
 
-  // Byte offsets of this thread's rows in a unit. K: tokens g and g + 8, 16-byte
-  // chunks 2t, 2t + 1 (D = 128) or t; V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, D / 8
+  // Byte offsets of this thread's rows in a unit's first tile. K: tokens g and g + 8,
+  // 16-byte chunks 2t, 2t + 1 (D = 128) or t; V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, D / 8
   // bytes at g D / 8. All but the 8-byte V loads of D = 64 are free of conflicts.
   uint32_t k_off[2], v_off[4];
   if (D == 128) {
@@ -351,79 +359,35 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       v_off[x] = C::kHalf + r * 128 + ((((x & 1) * 4 + (g >> 1)) ^ r) << 4) + (g & 1) * 8;
     }
   }
+  constexpr int kTile = 16 * D;  // bytes from a unit's tile to its next
 
-  int item = -1, b = 0, h = 0, row0 = 0, len = 0, u = 0, u_first = 0;
+  int item = 0, b = 0, h = 0, row0 = 0, len = 0, u = 0, u_first = 0, left = 0, U = 0;
   uint32_t qf[NT][D / 16][2];
-  float sc[NT][2], acc[NT][D / 16][4], ref[NT][2], l[NT][2];
+  // shift = kLift - reference; O = acc * vref / F
+  float sc[NT][2], acc[NT][D / 16][4], ref[NT][2], shift[NT][2], l[NT][2], vref = 0.f, iref = 0.f;
   int lim[NT][2];
   float* scores = nullptr;
   bool ok = true;
 
-  for (int i = 0; n_units > 0; ++i) {
+  for (int i = 0; i < n_units; ++i) {
     if ((i & 31) == 0 && i > 0) {
       cur = nxt;
-      nxt = locate<D>(p, pre, xs + i + 32 + lane, xe);
+      nxt = locate<D, UT>(p, pre, xs + i + 32 + lane, xe);
       load_ranges<D>(p, nxt);
     }
-    const int next_item = i < n_units ? __shfl_sync(0xffffffffu, cur.item, i & 31) : -1;
-    if (next_item != item) {
-      if (item >= 0) {
-        // ---- leave the item: its output, or this warp's partial of it
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-          }
-        if (u_first == 0 && u == (len + kUnit - 1) / kUnit) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int rr = row0 + 8 * n + 2 * t + e;
-              const bool some = l[n][e] != 0.f;
-              if (p.lse && g == 0)  // rows past the last one weigh nothing
-                p.lse[static_cast<long long>(item) * (8 * NT) + 8 * n + 2 * t + e] =
-                    some && rr < p.rows ? ref[n][e] - kLift + log2f(l[n][e]) : INFINITY;
-              if (rr >= p.rows) continue;
-              const float inv = some ? 1.f / l[n][e] : 0.f;
-              uint16_t* dst = out_row<D>(p, b, h, rr) + g * (D / 8);
-#pragma unroll
-              for (int m = 0; m < D / 16; ++m)
-                store_bf16(dst + 2 * m, acc[n][m][e] * inv, acc[n][m][e + 2] * inv);
-            }
-        } else {
-          // slot 0 (more items follow, the ring is in use): global scratch; slot 1 (the
-          // warp's last item, all its units consumed): the ring
-          const int slot = 2 * warp + (i == n_units);
-          float* o = i == n_units
-                         ? reinterpret_cast<float*>(ring)
-                         : p.warp_o + (static_cast<long long>(cta) * kAttnWarps + warp) * 8 * NT * D;
-          if (lane == 0) s_item[slot] = item;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = 8 * n + 2 * t + e;
-              if (g == 0) s_ml[slot * 8 * NT + c] = make_float2(ref[n][e], l[n][e]);
-              float2* dst = reinterpret_cast<float2*>(o + c * D + g * (D / 8));
-#pragma unroll
-              for (int m = 0; m < D / 16; ++m) dst[m] = make_float2(acc[n][m][e], acc[n][m][e + 2]);
-            }
-        }
-      }
-      if (i == n_units) break;
+    if (left == 0) {
       // ---- enter the next item: q as B operands, in fp16 at a power of two per row
-      item = next_item;
+      item = __shfl_sync(0xffffffffu, cur.item, i & 31);
       u = u_first = __shfl_sync(0xffffffffu, cur.u, i & 31);
       b = item / p.items_per_b;
       const int it = item - b * p.items_per_b;
       h = it / p.RT;
       row0 = (it - h * p.RT) * 8 * NT;
       len = clamp_len(p, b);
+      U = (len + C::kUnit - 1) / C::kUnit;
+      left = min(U - u, n_units - i);
       scores = p.scores ? p.scores + static_cast<long long>(item) * p.cap * p.rs : nullptr;
+      vref = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = row0 + 8 * n + g;
@@ -463,6 +427,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
           const int rr = row0 + 8 * n + 2 * t + e;
           lim[n][e] = len - a.nq + min(rr, p.rows - 1) / p.G;  // last key of the row
           ref[n][e] = kLowest;
+          shift[n][e] = kLift - kLowest;
           l[n][e] = 0.f;
         }
 #pragma unroll
@@ -476,133 +441,229 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     issue(i + S - 1, i >> 5);
     const float kr = __shfl_sync(0xffffffffu, cur.kr, i & 31);
     const float vr = __shfl_sync(0xffffffffu, cur.vr, i & 31);
-    const bool there = __shfl_sync(0xffffffffu, cur.row, i & 31) >= 0;
-    ok = __all_sync(0xffffffffu, wait_bar(&bars[i % S], (i / S) & 1, abort_flag, kSiteKv8));
-    if (!ok) break;
-    const int tok0 = u * kUnit;
-    ++u;
+    const bool there = __float_as_uint(kr) != __float_as_uint(kMissing);
+    const bool here = wait_bar(&bars[i % S], (i / S) & 1, abort_flag, kSiteKv8);
+    const int tok0 = u * C::kUnit;
     const uint8_t* stage = ring + (i % S) * 2 * C::kHalf;
-    // two accumulators a row tile (even and odd steps): half the chain of dependent MMAs
-    float s[NT][4], s2[NT][4];
+    float x[UT][NT][4];  // scores, then their exponents log2 p
+#pragma unroll
+    for (int y = 0; y < UT; ++y)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[y][n][e] = 0.f;
+    float x2[NT][4];  // one tile a unit: its odd steps, for half the chain of dependent MMAs
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) x2[n][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-      const uint4 ka = *reinterpret_cast<const uint4*>(stage + (k_off[0] ^ (j << 4)));
-      const uint4 kb = *reinterpret_cast<const uint4*>(stage + (k_off[1] ^ (j << 4)));
-      const uint32_t k0[4] = {ka.x, ka.y, ka.z, ka.w}, k1[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t a0, a1, a2, a3;
-        widen<FMT>(k0[w], a0, a2);
-        widen<FMT>(k1[w], a1, a3);
+      for (int y = 0; y < UT; ++y) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(stage + y * kTile + (k_off[0] ^ (j << 4)));
+        const uint4 kb = *reinterpret_cast<const uint4*>(stage + y * kTile + (k_off[1] ^ (j << 4)));
+        const uint32_t k0[4] = {ka.x, ka.y, ka.z, ka.w}, k1[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (w & 1)
-            mma16816(s2[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], s2[n]);
-          else
-            mma16816(s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], s[n]);
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          widen<FMT>(k0[w], a0, a2);
+          widen<FMT>(k1[w], a1, a3);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float(&d)[4] = UT == 1 && (w & 1) ? x2[n] : x[y][n];
+            mma16816(d, a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], d);
+          }
+        }
       }
     }
+    if (UT == 1)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[0][n][e] += x2[n][e];
     uint32_t v[4][D / 32];
+    auto load_v = [&](int y) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (D == 128) {
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + v_off[x]);
-        v[x][0] = w.x; v[x][1] = w.y; v[x][2 % (D / 32)] = w.z; v[x][3 % (D / 32)] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(stage + v_off[x]);
-        v[x][0] = w.x; v[x][1] = w.y;
+      for (int k = 0; k < 4; ++k) {
+        if (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + y * kTile + v_off[k]);
+          v[k][0] = w.x; v[k][1] = w.y; v[k][2 % (D / 32)] = w.z; v[k][3 % (D / 32)] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + y * kTile + v_off[k]);
+          v[k][0] = w.x; v[k][1] = w.y;
+        }
       }
-    }
+    };
+    load_v(0);  // before the votes: its latency passes behind the softmax
     // keys up to len - nq are seen by every row
-    const bool edge = tok0 + kUnit - 1 > len - a.nq || !there;
-    uint32_t pb[NT][2];
-    float vf[NT][2];
-    if (edge) {  // bytes behind the last token may hold anything, NaN codes among it
-      const int left = there ? len - tok0 : 0;
+    const bool edge = tok0 + C::kUnit - 1 > len - a.nq || !there;
+    // V's ranges: P carries vr / vref (at most 1 and at least 2^-10, so that fp16 holds it as
+    // it would hold P) and O accumulates in the products; vref moves when a range leaves that
+    // window. Infinite and NaN ranges stay out of vref: they are for their rows alone.
+    if ((vr > vref || (vr < vref * kFar && vr > vref * kFarthest)) && vr <= 3.4028234e38f) {
+      const float f = vref / vr;
+      vref = vr;
+      iref = 1.f / vr;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (2 * t + (x & 1) + 8 * (x >> 1) >= left)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) v[x][w] = 0;
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[n][m][e] *= f;
     }
+    const float rho = vr == vref ? 1.f : vref > 1e-30f ? vr * iref : vref > 0.f ? vr / vref : vr;
+    bool over = !here;
+    float f[NT][2], pv[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float f0 = sc[n][0] * kr, f1 = sc[n][1] * kr;
-      s[n][0] = (s[n][0] + s2[n][0]) * f0;
-      s[n][1] = (s[n][1] + s2[n][1]) * f1;
-      s[n][2] = (s[n][2] + s2[n][2]) * f0;
-      s[n][3] = (s[n][3] + s2[n][3]) * f1;
-      vf[n][0] = vf[n][1] = vr * (1.f / full<FMT>());
-      if (edge) {
-        // tokens of the unit that each of the thread's rows sees
+      f[n][0] = sc[n][0] * kr;
+      f[n][1] = sc[n][1] * kr;
+      pv[n][0] = pv[n][1] = rho;
+      if (edge) {  // tokens of the unit that each of the thread's rows sees
         const int see0 = there ? lim[n][0] - tok0 + 1 : 0, see1 = there ? lim[n][1] - tok0 + 1 : 0;
-        if (g >= see0) s[n][0] = -INFINITY;
-        if (g >= see1) s[n][1] = -INFINITY;
-        if (g + 8 >= see0) s[n][2] = -INFINITY;
-        if (g + 8 >= see1) s[n][3] = -INFINITY;
         // a row that sees nothing of the unit takes nothing from it, not even a NaN range
-        if (see0 <= 0) vf[n][0] = 0.f;
-        if (see1 <= 0) vf[n][1] = 0.f;
+        if (see0 <= 0) pv[n][0] = 0.f;
+        if (see1 <= 0) pv[n][1] = 0.f;
+#pragma unroll
+        for (int y = 0; y < UT; ++y) {
+          // (a score that is masked stands as -inf whatever its factor is)
+          x[y][n][0] = g + 16 * y >= see0 ? -INFINITY : x[y][n][0] * f[n][0];
+          x[y][n][1] = g + 16 * y >= see1 ? -INFINITY : x[y][n][1] * f[n][1];
+          x[y][n][2] = g + 16 * y + 8 >= see0 ? -INFINITY : x[y][n][2] * f[n][0];
+          x[y][n][3] = g + 16 * y + 8 >= see1 ? -INFINITY : x[y][n][3] * f[n][1];
+        }
+        f[n][0] = f[n][1] = 1.f;
       }
-      if (scores && 8 * n + 2 * t < p.rs) {
-        float* at = scores + (static_cast<long long>(tok0) + g) * p.rs + 8 * n + 2 * t;
-        if (tok0 + g < len) *reinterpret_cast<float2*>(at) = make_float2(s[n][0], s[n][1]);
-        if (tok0 + g + 8 < len)
-          *reinterpret_cast<float2*>(at + 8 * p.rs) = make_float2(s[n][2], s[n][3]);
+#pragma unroll
+      for (int y = 0; y < UT; ++y) {
+        if (scores && 8 * n + 2 * t < p.rs) {
+          const int tok = tok0 + 16 * y + g;
+          float* at = scores + static_cast<long long>(tok) * p.rs + 8 * n + 2 * t;
+          if (tok < len)
+            *reinterpret_cast<float2*>(at) = make_float2(x[y][n][0] * f[n][0], x[y][n][1] * f[n][1]);
+          if (tok + 8 < len)
+            *reinterpret_cast<float2*>(at + 8 * p.rs) =
+                make_float2(x[y][n][2] * f[n][0], x[y][n][3] * f[n][1]);
+        }
+        over = over || fmaxf(fmaf(fmaxf(x[y][n][0], x[y][n][2]), f[n][0], shift[n][0]),
+                             fmaf(fmaxf(x[y][n][1], x[y][n][3]), f[n][1], shift[n][1])) >
+                           kLift + kSlack;
       }
-      const float over = fmaxf(fmaxf(s[n][0], s[n][2]) - ref[n][0],
-                               fmaxf(s[n][1], s[n][3]) - ref[n][1]);
-      if (__any_sync(0xffffffffu, over > kSlack)) {
+    }
+    if (__any_sync(0xffffffffu, over)) {
+      if (__any_sync(0xffffffffu, !here)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float m = fmaxf(s[n][e], s[n][e + 2]);
+          float m = fmaxf(x[0][n][e], x[0][n][e + 2]);
+          if (UT == 2) m = fmaxf(m, fmaxf(x[UT - 1][n][e], x[UT - 1][n][e + 2]));
+          m *= f[n][e];
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
           m = fmaxf(m, ref[n][e]);
-          const float f = ex2(ref[n][e] - m);
+          const float k = ex2(ref[n][e] - m);
           ref[n][e] = m;
-          l[n][e] *= f;
+          shift[n][e] = kLift - m;
+          l[n][e] *= k;
 #pragma unroll
           for (int m2 = 0; m2 < D / 16; ++m2) {
-            acc[n][m2][e] *= f;
-            acc[n][m2][e + 2] *= f;
+            acc[n][m2][e] *= k;
+            acc[n][m2][e + 2] *= k;
           }
         }
-      }
-      float pr[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = ex2(s[n][e] - (ref[n][e & 1] - kLift));
-      l[n][0] += pr[0] + pr[2];
-      l[n][1] += pr[1] + pr[3];
-      pb[n][0] = transpose8x8(pack_half(pr[0], pr[1]));
-      pb[n][1] = transpose8x8(pack_half(pr[2], pr[3]));
     }
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t pb[UT][NT][2];
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
+    for (int y = 0; y < UT; ++y)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t x01 = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
-        const uint32_t x23 = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
+      for (int n = 0; n < NT; ++n) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pr[e] = ex2(fmaf(x[y][n][e], f[n][e & 1], shift[n][e & 1]));
+        l[n][0] += pr[0] + pr[2];
+        l[n][1] += pr[1] + pr[3];
+        pb[y][n][0] = transpose8x8(pack_half(pr[0] * pv[n][0], pr[1] * pv[n][1]));
+        pb[y][n][1] = transpose8x8(pack_half(pr[2] * pv[n][0], pr[3] * pv[n][1]));
+      }
+#pragma unroll
+    for (int y = 0; y < UT; ++y) {
+      if (y > 0) load_v(y);
+      if (edge) {  // bytes behind the last token may hold anything, NaN codes among it
+        const int rest = there ? len - tok0 - 16 * y : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (2 * t + (k & 1) + 8 * (k >> 1) >= rest)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) v[k][w] = 0;
+      }
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m) {
+        const uint32_t x01 = __byte_perm(v[0][m / 2], v[1][m / 2], m & 1 ? 0x7362 : 0x5140);
+        const uint32_t x23 = __byte_perm(v[2][m / 2], v[3][m / 2], m & 1 ? 0x7362 : 0x5140);
         uint32_t a0, a1, a2, a3;
         widen<FMT>(x01, a0, a1);
         widen<FMT>(x23, a2, a3);
-        const int m = 2 * w + half;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float d[4];
-          mma16816(d, a0, a1, a2, a3, pb[n][0], pb[n][1], zero);
-          acc[n][m][0] = fmaf(d[0], vf[n][0], acc[n][m][0]);
-          acc[n][m][1] = fmaf(d[1], vf[n][1], acc[n][m][1]);
-          acc[n][m][2] = fmaf(d[2], vf[n][0], acc[n][m][2]);
-          acc[n][m][3] = fmaf(d[3], vf[n][1], acc[n][m][3]);
-        }
+        for (int n = 0; n < NT; ++n)
+          mma16816(acc[n][m], a0, a1, a2, a3, pb[y][n][0], pb[y][n][1], acc[n][m]);
       }
+    }
+    ++u;
+    if (--left > 0) continue;
+
+    // ---- leave the item: its output, or this warp's partial of it
+    const float vs = vref * (1.f / full<FMT>());
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+      }
+    if (u_first == 0 && u == U) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = row0 + 8 * n + 2 * t + e;
+          const bool some = l[n][e] != 0.f;
+          if (p.lse && g == 0)  // rows past the last one weigh nothing
+            p.lse[static_cast<long long>(item) * (8 * NT) + 8 * n + 2 * t + e] =
+                some && rr < p.rows ? ref[n][e] - kLift + log2f(l[n][e]) : INFINITY;
+          if (rr >= p.rows) continue;
+          const float inv = some ? 1.f / l[n][e] : 0.f;
+          uint16_t* dst = out_row<D>(p, b, h, rr) + g * (D / 8);
+#pragma unroll
+          for (int m = 0; m < D / 16; ++m)
+            store_bf16(dst + 2 * m, acc[n][m][e] * vs * inv, acc[n][m][e + 2] * vs * inv);
+        }
+    } else {
+      // slot 0 (more items follow, the ring is in use): global scratch; slot 1 (the
+      // warp's last item, all its units consumed): the ring
+      const bool last = i + 1 == n_units;
+      const int slot = 2 * warp + last;
+      float* o = last ? reinterpret_cast<float*>(ring)
+                      : p.warp_o + (static_cast<long long>(cta) * W + warp) * 8 * NT * D;
+      if (lane == 0) s_item[slot] = item;
+      __syncwarp();  // every lane has read the last unit
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = 8 * n + 2 * t + e;
+          if (g == 0) s_ml[slot * 8 * NT + c] = make_float2(ref[n][e], l[n][e]);
+          float2* dst = reinterpret_cast<float2*>(o + c * D + g * (D / 8));
+#pragma unroll
+          for (int m = 0; m < D / 16; ++m)
+            dst[m] = make_float2(acc[n][m][e] * vs, acc[n][m][e + 2] * vs);
+        }
     }
   }
   if (!ok) {  // gave up on a load: let those in flight land before the memory goes away
@@ -614,7 +675,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   // Join the warps' partials of each item, in order. A warp takes one column (row of
   // the item) of one item at a time, D / 4 lanes a column; the loads of all its
   // partials go out together.
-  constexpr int kSlots = 2 * kAttnWarps, kLanes = D / 4, kCols = 32 / kLanes;
+  constexpr int kSlots = 2 * W, kLanes = D / 4, kCols = 32 / kLanes;
   int it_of[kSlots];
 #pragma unroll
   for (int k = 0; k < kSlots / 4; ++k) {
@@ -633,7 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     }
   }
   const int tasks = __popc(first) * (8 * NT / kCols), sub = lane / kLanes, d4 = lane % kLanes;
-  for (int task = warp; task < tasks; task += kAttnWarps) {
+  for (int task = warp; task < tasks; task += W) {
     const int c = (task % (8 * NT / kCols)) * kCols + sub;
     uint32_t f = first;
     for (int k = task / (8 * NT / kCols); k > 0; --k) f &= f - 1;
@@ -662,7 +723,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
         const int s = k0 + k;
         if (it_of[s] == it_id) {
           const float* src = s & 1 ? reinterpret_cast<const float*>(smem + (s >> 1) * C::kWarpRing)
-                                   : p.warp_o + (static_cast<long long>(cta) * kAttnWarps + (s >> 1)) *
+                                   : p.warp_o + (static_cast<long long>(cta) * W + (s >> 1)) *
                                                     8 * NT * D;
           v[k] = *reinterpret_cast<const float4*>(src + c * D + 4 * d4);
         }
@@ -809,7 +870,7 @@ AttnLayout attn_layout(int B, int nq, int Hq, int Hkv, int D, int max_pages, int
   l.part_o = 0;
   l.part_ml = al(slots * D * 4);
   l.warp_o = l.part_ml + al(slots * 8);
-  l.close = l.warp_o + al(slots / 2 * kAttnWarps * D * 4);
+  l.close = l.warp_o + al(slots / 2 * kWarps * D * 4);
   l.lse = l.close + al(2LL * kMaxSms * 16);
   l.scores = l.lse + (with_weights ? al(items * 8 * l.NT * 4) : 0);
   l.rs = (std::min(rows, 8 * l.NT) + 3) / 4 * 4;
@@ -818,11 +879,11 @@ AttnLayout attn_layout(int B, int nq, int Hq, int Hkv, int D, int max_pages, int
 }
 
 // The codes of a pool as rows of 128 bytes, one unit a box, 128-byte swizzle.
-template <int D>
+template <int D, int UT>
 int encode_codes(CUtensorMap* m, const void* codes, const Kv8Cache& c) {
   const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(c.num_pages) * c.Hkv * c.page * D / 128};
   const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, kUnit * D / 128};
+  const cuuint32_t box[2] = {128, 16 * UT * D / 128};
   const cuuint32_t estr[2] = {1, 1};
   return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box,
                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -832,23 +893,25 @@ int encode_codes(CUtensorMap* m, const void* codes, const Kv8Cache& c) {
              : TM_ERR_CUDA;
 }
 
-template <int D, int FMT, int NT>
+template <int D, int FMT, int NT, int UT>
 int attn_run(AttnP& p, DeviceInfo* di) {
-  using C = AttnCfg<D, NT>;
+  using C = AttnCfg<D, NT, UT>;
   const Kv8AttnArgs& a = p.a;
-  constexpr int kidx = (D == 128) * 4 + (FMT == TM_KV_E4M3) * 2 + (NT == 2);
-  if (int rc = set_smem_once(di->kv8_attr_set[kidx], attn_kernel8<D, FMT, NT>,
+  constexpr int kidx = (D == 128) * 8 + (FMT == TM_KV_E4M3) * 4 + (NT == 2) * 2 + (UT == 2);
+  if (int rc = set_smem_once(di->kv8_attr_set[kidx], attn_kernel8<D, FMT, NT, UT>,
                              C::kSmem + 4 * kMaxAttnBatch))
     return rc;
   CUtensorMap tk, tv;
-  if (encode_codes<D>(&tk, a.c.k8, a.c) || encode_codes<D>(&tv, a.c.v8, a.c)) return TM_ERR_CUDA;
+  if (encode_codes<D, UT>(&tk, a.c.k8, a.c) || encode_codes<D, UT>(&tv, a.c.v8, a.c))
+    return TM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
   // a CTA for every unit a warp could get, at most what is resident at once
-  const long long units = static_cast<long long>(a.B) * p.items_per_b * ((p.cap + kUnit - 1) / kUnit);
-  p.grid = static_cast<int>(std::min<long long>(std::min(di->sms, kMaxSms) * (NT == 1 ? 2 : 1),
-                                                (units + kAttnWarps - 1) / kAttnWarps));
-  if (launch_early(attn_kernel8<D, FMT, NT>, dim3(p.grid), kAttnThreads, C::kSmem + a.B * 4, st, 1, tk,
-                   tv, p))
+  const long long units =
+      static_cast<long long>(a.B) * p.items_per_b * ((p.cap + C::kUnit - 1) / C::kUnit);
+  p.grid = static_cast<int>(
+      std::min<long long>(std::min(di->sms, kMaxSms) * C::kCtas, (units + kWarps - 1) / kWarps));
+  if (launch_early(attn_kernel8<D, FMT, NT, UT>, dim3(p.grid), C::kThreads, C::kSmem + a.B * 4, st, 1,
+                   tk, tv, p))
     return TM_ERR_CUDA;
   const dim3 grid(p.grid, 8 * NT);
   if (launch_early(combine_kernel<D, NT>, grid, 128, 0, st, 1, p)) return TM_ERR_CUDA;
@@ -861,7 +924,10 @@ int attn_run(AttnP& p, DeviceInfo* di) {
 
 template <int D, int FMT>
 int attn_nt(AttnP& p, int NT, DeviceInfo* di) {
-  return NT == 1 ? attn_run<D, FMT, 1>(p, di) : attn_run<D, FMT, 2>(p, di);
+  constexpr int kOne = D == 64 ? 2 : 1;  // tiles of a unit with one row tile
+  if (p.a.c.page >= 32)
+    return NT == 1 ? attn_run<D, FMT, 1, kOne>(p, di) : attn_run<D, FMT, 2, 2>(p, di);
+  return NT == 1 ? attn_run<D, FMT, 1, 1>(p, di) : attn_run<D, FMT, 2, 1>(p, di);
 }
 
 }  // namespace
