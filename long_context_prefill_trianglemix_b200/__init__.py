@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import Any, NamedTuple
 
 import numpy as np
 
@@ -141,27 +142,33 @@ def _ptr(x):
 
 
 _current_stream = None
+_device = None
 
 
 def _find_current_stream():
-    """A function that gives the handle of torch's current stream. torch.cuda.current_stream()
-    builds a Stream object first, 3.3 us of a short call's 10 us on the host; the raw handle
-    (0.2 us) is taken where torch gives it."""
-    global _current_stream
+    """Sets _current_stream and _device, functions that give the handle of torch's current stream
+    and the number of its current device; returns the latter. torch.cuda.current_stream() builds
+    a Stream object first, 3.3 us of a short call's 10 us on the host; the raw handle (0.2 us) is
+    taken where torch gives it."""
+    global _current_stream, _device
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     device = getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.current_stream()  # initialises CUDA
     if raw is None or device is None:
         _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        _device = torch.cuda.current_device
     else:
-        torch.cuda.current_stream()  # initialises CUDA
         _current_stream = lambda: raw(device())  # noqa: E731
-    return _current_stream
+        _device = device
+    return _device
 
 
 def _stream(s):
     if s is None:
-        return (_current_stream or _find_current_stream())()
+        if _current_stream is None:
+            _find_current_stream()
+        return _current_stream()
     if hasattr(s, "cuda_stream"):
         return s.cuda_stream
     return int(s)
@@ -364,13 +371,34 @@ def tm_debug_inject_stall(q, k, v, o, B, Hq, Hkv, N, D, scale, S, W, L, stream=N
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, Hkv, N, D, scale, S, W, L, _stream(stream)))
 
 
+def _device_ptrs(*xs):
+    """Addresses of the arguments; a tensor has to lie on the current device (a kernel that
+    reads another device's or the host's memory faults)."""
+    out, here = [], None
+    for x in xs:
+        if x is None:
+            out.append(None)
+            continue
+        try:
+            device = x.get_device()  # -1: the host
+        except AttributeError:
+            out.append(int(x))
+            continue
+        if device != here:
+            if here is not None or device < 0 or device != (_device or _find_current_stream())():
+                raise ValueError(f"a tensor on {x.device}, which is not the current CUDA device")
+            here = device
+        out.append(x.data_ptr())
+    return out
+
+
 def tm_rope_fwd(q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_stride,
                 k_out_stride, rot, layout, inverse, inv_freq, mscale, positions, first,
                 stream=None):
+    q, q_out, k, k_out, f, pos = _device_ptrs(q, q_out, k, k_out, inv_freq, positions)
     return _check("tm_rope_fwd", lib().tm_rope_fwd(
-        _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), B, N, Hq, Hkv, D, q_stride, q_out_stride,
-        k_stride, k_out_stride, rot, layout, int(inverse), _ptr(inv_freq), mscale,
-        _ptr(positions), first, _stream(stream)))
+        q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_stride, k_out_stride, rot,
+        layout, int(inverse), f, mscale, pos, first, _stream(stream)))
 
 
 def tm_rope_inv_freq(rot, base, factor=1.0, trained_len=1.0, low_turns=0.0,
@@ -384,19 +412,22 @@ def tm_rope_inv_freq(rot, base, factor=1.0, trained_len=1.0, low_turns=0.0,
 
 def tm_kv8_append(k, v, k_stride, v_stride, B, n_src, n, Hkv, D, counts, index, lens, table,
                   max_pages, k8, v8, k_range, v_range, num_pages, page, format, stream=None):
+    k, v, counts, index, lens, table, k8, v8, k_range, v_range = _device_ptrs(
+        k, v, counts, index, lens, table, k8, v8, k_range, v_range)
     return _check("tm_kv8_append", lib().tm_kv8_append(
-        _ptr(k), _ptr(v), k_stride, v_stride, B, n_src, n, Hkv, D, _ptr(counts), _ptr(index),
-        _ptr(lens), _ptr(table), max_pages, _ptr(k8), _ptr(v8), _ptr(k_range), _ptr(v_range),
-        num_pages, page, format, _stream(stream)))
+        k, v, k_stride, v_stride, B, n_src, n, Hkv, D, counts, index, lens, table, max_pages, k8,
+        v8, k_range, v_range, num_pages, page, format, _stream(stream)))
 
 
 def tm_kv8_compact(index, keep, kept, lens, B, Hkv, D, table, max_pages, new_table, new_max_pages,
                    k8, v8, k_range, v_range, num_pages, page, format, weights, weights_stride,
                    new_weights, new_weights_stride, stream=None):
+    index, kept, lens, table, new_table, k8, v8, k_range, v_range, weights, new_weights = \
+        _device_ptrs(index, kept, lens, table, new_table, k8, v8, k_range, v_range, weights,
+                     new_weights)
     return _check("tm_kv8_compact", lib().tm_kv8_compact(
-        _ptr(index), keep, _ptr(kept), _ptr(lens), B, Hkv, D, _ptr(table), max_pages,
-        _ptr(new_table), new_max_pages, _ptr(k8), _ptr(v8), _ptr(k_range), _ptr(v_range),
-        num_pages, page, format, _ptr(weights), weights_stride, _ptr(new_weights),
+        index, keep, kept, lens, B, Hkv, D, table, max_pages, new_table, new_max_pages, k8, v8,
+        k_range, v_range, num_pages, page, format, weights, weights_stride, new_weights,
         new_weights_stride, _stream(stream)))
 
 
@@ -410,10 +441,11 @@ def tm_kv8_attn_workspace_size(B, nq, Hq, Hkv, D, max_pages, page, with_weights)
 def tm_kv8_attn_fwd(q, o, B, nq, Hq, Hkv, D, scale, k8, v8, k_range, v_range, num_pages, page,
                     format, table, max_pages, lens, weights, weights_stride, accumulate,
                     workspace, workspace_bytes, stream=None):
+    q, o, k8, v8, k_range, v_range, table, lens, weights, workspace = _device_ptrs(
+        q, o, k8, v8, k_range, v_range, table, lens, weights, workspace)
     return _check("tm_kv8_attn_fwd", lib().tm_kv8_attn_fwd(
-        _ptr(q), _ptr(o), B, nq, Hq, Hkv, D, scale, _ptr(k8), _ptr(v8), _ptr(k_range),
-        _ptr(v_range), num_pages, page, format, _ptr(table), max_pages, _ptr(lens),
-        _ptr(weights), weights_stride, int(accumulate), _ptr(workspace), workspace_bytes,
+        q, o, B, nq, Hq, Hkv, D, scale, k8, v8, k_range, v_range, num_pages, page, format, table,
+        max_pages, lens, weights, weights_stride, int(accumulate), workspace, workspace_bytes,
         _stream(stream)))
 
 
@@ -426,16 +458,18 @@ def tm_key_weights_workspace_size(B, Hq, Hkv, N, D, L) -> int:
 
 def tm_key_weights_fwd(q, k, B, Hq, Hkv, N, D, scale, L, lens, weights, weights_stride,
                        accumulate, workspace, workspace_bytes, stream=None):
+    q, k, lens, weights, workspace = _device_ptrs(q, k, lens, weights, workspace)
     return _check("tm_key_weights_fwd", lib().tm_key_weights_fwd(
-        _ptr(q), _ptr(k), B, Hq, Hkv, N, D, scale, L, _ptr(lens), _ptr(weights), weights_stride,
-        int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
+        q, k, B, Hq, Hkv, N, D, scale, L, lens, weights, weights_stride, int(accumulate),
+        workspace, workspace_bytes, _stream(stream)))
 
 
 def tm_kv_select(weights, weights_stride, lens, B, H, n, keep, sinks, recent, index, kept=None,
                  stream=None):
+    weights, lens, index, kept = _device_ptrs(weights, lens, index, kept)
     return _check("tm_kv_select", lib().tm_kv_select(
-        _ptr(weights), weights_stride, _ptr(lens), B, H, n, keep, sinks, recent, _ptr(index),
-        _ptr(kept), _stream(stream)))
+        weights, weights_stride, lens, B, H, n, keep, sinks, recent, index, kept,
+        _stream(stream)))
 
 
 def tm_get_device_status(stream=None) -> int:
@@ -485,3 +519,193 @@ def trianglemix_attention(q, k, v, S, W, L, layer, tri_start, scale=None, out=No
                             1.0 / math.sqrt(D) if scale is None else scale, S, W, L, layer,
                             tri_start, stream)
     return o
+
+
+# The operators around the attention, on torch tensors. Token counts and tables are int32 CUDA
+# tensors, k and v bf16; shapes and types are checked here, ranges of values on the device.
+
+def _need(x, name, dtype, *shape):
+    """x has this dtype and shape (None: any size) and is contiguous."""
+    if x.dtype != dtype:
+        raise ValueError(f"{name} is {x.dtype}, not {dtype}")
+    if x.dim() != len(shape) or any(n is not None and x.shape[i] != n for i, n in enumerate(shape)):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, not {shape}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return x
+
+
+def _token_rows(x, name, D=None):
+    """Token stride of bf16 [B, N, H, D] rows whose heads are contiguous (a slice of a packed
+    projection is)."""
+    import torch
+    if x.dtype != torch.bfloat16 or x.dim() != 4 or (D is not None and x.shape[3] != D):
+        raise ValueError(f"{name}: {x.dtype} {tuple(x.shape)} is not bf16 [B, N, H, {D or 'D'}]")
+    B, N, H, D = x.shape
+    if (D > 1 and x.stride(3) != 1) or (H > 1 and x.stride(2) != D):
+        raise ValueError(f"{name}: the heads of a token are not contiguous")
+    if N > 1:
+        stride = x.stride(1)
+        if B > 1 and x.stride(0) != N * stride:
+            raise ValueError(f"{name}: the batches do not follow each other")
+    else:
+        stride = x.stride(0) if B > 1 else H * D
+    return stride
+
+
+def rope(q, k, inv_freq, positions=None, first=0, rot=None, interleaved=False, mscale=1.0,
+         inverse=False, out=None, stream=None):
+    """Rotary positions of bf16 q [B, N, Hq, D] and k [B, N, Hkv, D] (either may be None, both
+    may be slices of a packed projection). ``inv_freq``: rot / 2 doubles on the device
+    (tm_rope_inv_freq). ``out``: the pair to write to, (q, k) themselves to turn in place."""
+    import torch
+    x = q if q is not None else k
+    B, N, _, D = x.shape
+    rot = D if rot is None else rot
+    _need(inv_freq, "inv_freq", torch.float64, rot // 2)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, B, N)
+    outs = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            for t in (q, k)] if out is None else list(out)
+    H, st = [], []
+    for t, o, name in ((q, outs[0], "q"), (k, outs[1], "k")):
+        if t is None:
+            H.append(0)
+            st += [0, 0]
+            continue
+        if t.shape[:2] != (B, N) or t.shape[3] != D or o.shape != t.shape:
+            raise ValueError(f"{name}: {tuple(t.shape)} and {tuple(o.shape)} do not fit")
+        H.append(t.shape[2])
+        st += [_token_rows(t, name), _token_rows(o, name + "'s output")]
+    tm_rope_fwd(q, outs[0], k, outs[1], B, N, H[0], H[1], D, *st, rot, int(bool(interleaved)),
+                inverse, inv_freq, mscale, positions, first, stream)
+    return tuple(outs)
+
+
+class Kv8Cache(NamedTuple):
+    """A paged 8-bit cache: codes [num_pages, Hkv, page, D] (int8 or float8_e4m3fn) and their
+    blocks' ranges [num_pages, Hkv]."""
+    k8: Any
+    v8: Any
+    k_range: Any
+    v_range: Any
+
+    @staticmethod
+    def empty(num_pages, Hkv, page, D, format=TM_KV_INT8, device="cuda"):
+        import torch
+        dtype = torch.int8 if format == TM_KV_INT8 else torch.float8_e4m3fn
+        codes = [torch.zeros((num_pages, Hkv, page, D), dtype=torch.int8, device=device).view(dtype)
+                 for _ in range(2)]
+        return Kv8Cache(*codes, *(torch.zeros((num_pages, Hkv), device=device) for _ in range(2)))
+
+    def _args(self):
+        """(codes and ranges..., num_pages, page, format), checked."""
+        import torch
+        n, H, page, D = self.k8.shape
+        _need(self.k8, "k8", self.k8.dtype, n, H, page, D)
+        _need(self.v8, "v8", self.k8.dtype, n, H, page, D)
+        _need(self.k_range, "k_range", torch.float32, n, H)
+        _need(self.v_range, "v_range", torch.float32, n, H)
+        formats = {torch.int8: TM_KV_INT8, torch.float8_e4m3fn: TM_KV_E4M3}
+        if self.k8.dtype not in formats:
+            raise ValueError(f"codes of {self.k8.dtype}")
+        return (self.k8, self.v8, self.k_range, self.v_range, n, page, formats[self.k8.dtype])
+
+
+def kv8_append(cache, k, v, lens, table, counts=None, index=None, stream=None):
+    """Store bf16 k, v [B, n, Hkv, D] behind the lens[b] tokens a sequence holds (lens is not
+    changed); only the first counts[b], or the rows index [B, Hkv, n] of each head."""
+    import torch
+    _, H, _, D = cache.k8.shape
+    B, n_src = k.shape[:2]
+    ks, vs = _token_rows(k, "k", D), _token_rows(v, "v", D)
+    if v.shape != k.shape or k.shape[2] != H:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for {H} heads")
+    n = n_src
+    if index is not None:
+        n = _need(index, "index", torch.int32, B, H, None).shape[2]
+    if counts is not None:
+        _need(counts, "counts", torch.int32, B)
+    _need(lens, "lens", torch.int32, B)
+    _need(table, "table", torch.int32, B, None)
+    tm_kv8_append(k, v, ks, vs, B, n_src, n, H, D, counts, index, lens, table, table.shape[1],
+                  *cache._args(), stream)
+
+
+def kv8_attention(cache, q, lens, table, scale=None, weights=None, accumulate=False, out=None,
+                  workspace=None, stream=None):
+    """Attention of the last nq tokens, bf16 q [B, nq, Hq, D], over the cache; the weight of each
+    key into ``weights`` [B, Hkv, tokens] if given. A ``workspace`` (uint8) saves its allocation."""
+    import torch
+    B, nq, Hq, D = q.shape
+    _, H, page, Dc = cache.k8.shape
+    _need(q, "q", torch.bfloat16, B, nq, Hq, Dc)
+    _need(lens, "lens", torch.int32, B)
+    mp = _need(table, "table", torch.int32, B, None).shape[1]
+    if weights is not None:
+        _need(weights, "weights", torch.float32, B, H, None)
+    o = _need(_out(q, out), "out", torch.bfloat16, B, nq, Hq, D)
+    size = tm_kv8_attn_workspace_size(B, nq, Hq, H, D, mp, page, weights is not None)
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    tm_kv8_attn_fwd(q, o, B, nq, Hq, H, D, 1.0 / math.sqrt(D) if scale is None else scale,
+                    *cache._args(), table, mp, lens, weights,
+                    0 if weights is None else weights.shape[2], accumulate, workspace,
+                    workspace.numel() * workspace.element_size(), stream)
+    return o
+
+
+def key_weights(q, k, L, lens=None, scale=None, weights=None, accumulate=False, workspace=None,
+                stream=None):
+    """The attention weight each key of bf16 k [B, N, Hkv, D] receives from the last L queries of
+    q [B, N, Hq, D], [B, Hkv, N] (keys past a sequence's length stay as they are, 0 if new)."""
+    import torch
+    B, N, Hq, Hkv, D = _shapes(q, k)
+    _need(q, "q", torch.bfloat16, B, N, Hq, D)
+    _need(k, "k", torch.bfloat16, B, N, Hkv, D)
+    if lens is not None:
+        _need(lens, "lens", torch.int32, B)
+    if weights is None:
+        weights = torch.zeros((B, Hkv, N), device=q.device)
+    _need(weights, "weights", torch.float32, B, Hkv, None)
+    size = tm_key_weights_workspace_size(B, Hq, Hkv, N, D, L)
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    tm_key_weights_fwd(q, k, B, Hq, Hkv, N, D, 1.0 / math.sqrt(D) if scale is None else scale, L,
+                       lens, weights, weights.shape[2], accumulate, workspace,
+                       workspace.numel() * workspace.element_size(), stream)
+    return weights
+
+
+def kv_select(weights, keep, sinks=0, recent=0, lens=None, n=None, stream=None):
+    """(index [B, H, keep], kept [B]): the tokens to keep of weights [B, H, tokens], of which the
+    first n (all) or lens[b] are there."""
+    import torch
+    B, H, cap = _need(weights, "weights", torch.float32, None, None, None).shape
+    if lens is not None:
+        _need(lens, "lens", torch.int32, B)
+    index = torch.empty((B, H, keep), dtype=torch.int32, device=weights.device)
+    kept = torch.empty(B, dtype=torch.int32, device=weights.device)
+    tm_kv_select(weights, cap, lens, B, H, cap if n is None else n, keep, sinks, recent, index, kept,
+                 stream)
+    return index, kept
+
+
+def kv8_compact(cache, index, kept, lens, table, new_table, weights=None, new_weights=None,
+                stream=None):
+    """Move the kept tokens (index [B, Hkv, keep], kept [B]) from table's pages to new_table's,
+    and their weights along."""
+    import torch
+    _, H, _, D = cache.k8.shape
+    B, _, keep = _need(index, "index", torch.int32, None, H, None).shape
+    _need(kept, "kept", torch.int32, B)
+    _need(lens, "lens", torch.int32, B)
+    _need(table, "table", torch.int32, B, None)
+    _need(new_table, "new_table", torch.int32, B, None)
+    for w, name in ((weights, "weights"), (new_weights, "new_weights")):
+        if w is not None:
+            _need(w, name, torch.float32, B, H, None)
+    tm_kv8_compact(index, keep, kept, lens, B, H, D, table, table.shape[1], new_table,
+                   new_table.shape[1], *cache._args(), weights,
+                   0 if weights is None else weights.shape[2], new_weights,
+                   0 if new_weights is None else new_weights.shape[2], stream)

@@ -6,16 +6,18 @@
 // codes once (2 D bytes a token and kv head) bounds it; everything else is
 // arranged so that the loads never wait for anything:
 //
-// - A unit is 16 tokens of one (page, head): 16 rows of D codes, contiguous. All
+// - A unit is 16 or 32 tokens of one (page, head): rows of D codes, contiguous. All
 //   units of all sequences and heads form one line, cut into equal parts for
 //   the CTAs and again for their warps, so ragged batches are balanced to a
 //   unit. A warp walks its part alone, across items, fed by its own ring of TMA
 //   loads (its lanes hold where the next 32 to 64 units lie).
 // - The codes are the A operand of m16n8k16 products and the (at most 8 NT) rows
 //   the n side, so a group of 4 or 8 q heads wastes no matrix work: S^T = K Q^T
-//   (16 tokens x 8 rows), O^T += V^T P^T (16 dims x 8 rows). The order of the
-//   contraction index is free, so each thread loads 16 contiguous bytes of its
-//   token rows and uses them in place; P^T goes from accumulator to operand
+//   (16 tokens x 8 rows), O^T += V^T P^T (16 dims x 8 rows). mma.sync and not tcgen05:
+//   at 8 rows the products take a tenth of the tensor pipe, and operands that are
+//   converted from 8 bits on their way are in registers, not in shared memory. The
+//   order of the contraction index is free, so each thread loads 16 contiguous bytes
+//   of its token rows and uses them in place; P^T goes from accumulator to operand
 //   layout by an 8x8 transpose (movmatrix).
 // - Codes become fp16 exactly (int8 by 1024 + u in the low mantissa bits, e4m3 by
 //   the conversion instruction). q becomes fp16 after an exact scaling of the
@@ -23,9 +25,10 @@
 //   fp16's 11 bits hold bf16's 8, and elements 2^-29 of the largest or less are
 //   rounded by at most 2^-40 of it. Products and sums are fp32.
 // - P is fp16, scaled by 2^8 against the running reference and allowed to grow
-//   to 2^15, which leaves weights down to 2^-32 of the largest in fp16's range
-//   (rounding 2^-12 of each weight, below the bf16 output's 2^-9). The
-//   reference moves only when a score exceeds it by more than 7 (log2), so the
+//   to 2^15, and carries V's range, kept within 2^-10 of a reference of its own:
+//   weights down to 2^-22 of the largest keep fp16's 11 bits (rounding 2^-11 of each
+//   weight, below the bf16 output's 2^-8), less ones are off by 2^-33 of the largest.
+//   The reference moves only when a score exceeds it by more than 7 (log2), so the
 //   usual unit needs one vote and no rescale; m, l and O are fp32.
 //
 // Parts of an item (sequence, kv head, row tile) that end in one CTA are merged
@@ -44,7 +47,7 @@ constexpr int kMaxSms = 192;    // workspaces are sized for this many
 constexpr float kLift = 8.f;    // log2 of the scale of P against the reference
 constexpr float kSlack = 7.f;   // scores may exceed the reference by this
 constexpr float kFar = 0x1p-10f;  // P takes a V range in while it is this much of the reference
-constexpr float kFarthest = 0x1p-70f;  // (further down it adds nothing that fp32 would hold)
+constexpr float kFarthest = 0x1p-70f;  // (further below the largest it adds nothing fp32 would hold)
 constexpr float kLowest = -1.7e38f;
 
 struct AttnP {
@@ -134,13 +137,15 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& first, uint32_t& sec
   }
 }
 
-// UT tiles of 16 tokens make a unit. Two halve what a unit costs besides its codes
-// (under the power cap, where the clock falls to 1.6 GHz, instruction issue and not
-// memory bounds this kernel) but need registers or shared memory that one row tile of
-// D = 128 has a better use for: 16 warps an SM with one tile each took 337 us where 12
-// with two took 350 (8 sequences of 131072 tokens, e4m3). Each warp has a ring of S
-// units (K rows, then V rows, 128-byte swizzled by the TMA load): one unit loads while
-// another is computed; more in flight is slower (three deep 347 us, two deep 324).
+// UT tiles of 16 tokens make a unit. Two halve what a unit costs besides its codes but
+// need registers or shared memory that one row tile of D = 128 has a better use for:
+// 16 warps an SM with one tile each took 338 us where 12 with two took 350 (8 sequences
+// of 131072 tokens, e4m3). Under a sustained load the power cap brings the clock to
+// 1.5 to 1.6 GHz, where the conversions of int8 bound this kernel (378 us, 5.7 TB/s;
+// e4m3 338 us, 6.4 TB/s) and memory does not; in short runs both take 320 us (6.7 TB/s).
+// Each warp has a ring of S units (K rows, then V rows, 128-byte swizzled by the TMA
+// load): one unit loads while another is computed; more in flight is slower (three deep
+// 347 us, two deep 324 in short runs).
 template <int D, int NT, int UT>
 struct AttnCfg {
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // an SM, 128 and 255 registers a thread
@@ -364,7 +369,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
   int item = 0, b = 0, h = 0, row0 = 0, len = 0, u = 0, u_first = 0, left = 0, U = 0;
   uint32_t qf[NT][D / 16][2];
   // shift = kLift - reference; O = acc * vref / F
-  float sc[NT][2], acc[NT][D / 16][4], ref[NT][2], shift[NT][2], l[NT][2], vref = 0.f, iref = 0.f;
+  float sc[NT][2], acc[NT][D / 16][4], ref[NT][2], shift[NT][2], l[NT][2];
+  float vref = 0.f, iref = 0.f, vtop = 0.f;  // V's reference range, 1 / it, the largest so far
   int lim[NT][2];
   float* scores = nullptr;
   bool ok = true;
@@ -387,7 +393,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       U = (len + C::kUnit - 1) / C::kUnit;
       left = min(U - u, n_units - i);
       scores = p.scores ? p.scores + static_cast<long long>(item) * p.cap * p.rs : nullptr;
-      vref = 0.f;
+      vref = vtop = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = row0 + 8 * n + g;
@@ -482,28 +488,15 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[0][n][e] += x2[n][e];
-    uint32_t v[4][D / 32];
-    auto load_v = [&](int y) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + y * kTile + v_off[k]);
-          v[k][0] = w.x; v[k][1] = w.y; v[k][2 % (D / 32)] = w.z; v[k][3 % (D / 32)] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + y * kTile + v_off[k]);
-          v[k][0] = w.x; v[k][1] = w.y;
-        }
-      }
-    };
-    load_v(0);  // before the votes: its latency passes behind the softmax
     // keys up to len - nq are seen by every row
     const bool edge = tok0 + C::kUnit - 1 > len - a.nq || !there;
     // V's ranges: P carries vr / vref (at most 1 and at least 2^-10, so that fp16 holds it as
     // it would hold P) and O accumulates in the products; vref moves when a range leaves that
     // window. Infinite and NaN ranges stay out of vref: they are for their rows alone.
-    if ((vr > vref || (vr < vref * kFar && vr > vref * kFarthest)) && vr <= 3.4028234e38f) {
+    if ((vr > vref || (vr < vref * kFar && vr > vtop * kFarthest)) && vr <= 3.4028234e38f) {
       const float f = vref / vr;
       vref = vr;
+      vtop = fmaxf(vtop, vr);
       iref = 1.f / vr;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -593,7 +586,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       }
 #pragma unroll
     for (int y = 0; y < UT; ++y) {
-      if (y > 0) load_v(y);
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + y * kTile + v_off[k]);
+          v[k][0] = w.x; v[k][1] = w.y; v[k][2 % (D / 32)] = w.z; v[k][3 % (D / 32)] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + y * kTile + v_off[k]);
+          v[k][0] = w.x; v[k][1] = w.y;
+        }
+      }
       if (edge) {  // bytes behind the last token may hold anything, NaN codes among it
         const int rest = there ? len - tok0 - 16 * y : 0;
 #pragma unroll

@@ -200,3 +200,50 @@ def test_reference_rounding_is_the_formats():
     got = torch.from_numpy(x).to(torch.float8_e4m3fn).float().numpy()
     np.testing.assert_array_equal(ref.nearest(x, ref.E4M3), got)
     assert ref.nearest(2.5, ref.INT8) == 2 and ref.nearest(3.5, ref.INT8) == 4
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    """Before any CUDA call: a host tensor (a kernel would fault on it), other types and shapes."""
+    import torch
+    x = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
+    i32 = torch.zeros((1,), dtype=torch.int32)
+    table = torch.zeros((1, 2), dtype=torch.int32)
+    f = torch.zeros(32, dtype=torch.float64)
+    cache = tm.Kv8Cache.empty(4, 2, 16, 64, device="cpu")
+    with pytest.raises(ValueError, match="current CUDA device"):
+        tm.rope(x, x.clone(), f)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        tm.kv8_append(cache, x, x, i32, table)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        tm.kv8_attention(cache, x, i32, table)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        tm.key_weights(x, x, 2)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        tm.kv_select(torch.zeros((1, 2, 8)), 4)
+    bad = [lambda: tm.rope(x, x, f.float()), lambda: tm.rope(x, x, f[:30]),
+           lambda: tm.rope(x.float(), None, f), lambda: tm.rope(x, x[:, :3], f),
+           lambda: tm.rope(x, x, f, positions=torch.zeros((1, 4))),
+           lambda: tm.rope(x.transpose(2, 3), None, f[:1]),
+           lambda: tm.kv8_append(cache, x, x, i32.long(), table),
+           lambda: tm.kv8_append(cache, x[..., :32], x[..., :32], i32, table),
+           lambda: tm.kv8_append(cache, x, x[:, :2], i32, table),
+           lambda: tm.kv8_append(cache, x, x, i32, table[0]),
+           lambda: tm.kv8_append(cache, x, x, i32, table, index=torch.zeros((1, 1, 4), dtype=torch.int32)),
+           lambda: tm.kv8_append(cache, x, x, i32, table, counts=torch.zeros(2, dtype=torch.int32)),
+           lambda: tm.kv8_append(cache._replace(k_range=i32), x, x, i32, table),
+           lambda: tm.kv8_append(cache._replace(v8=cache.v8.float()), x, x, i32, table),
+           lambda: tm.kv8_attention(cache, x.float(), i32, table),
+           lambda: tm.kv8_attention(cache, x, i32, table, weights=torch.zeros((1, 1, 32))),
+           lambda: tm.key_weights(x, x.float(), 2),
+           lambda: tm.key_weights(x, x, 2, lens=torch.zeros(1)),
+           lambda: tm.kv_select(torch.zeros((1, 2, 8)).double(), 4),
+           lambda: tm.kv8_compact(cache, torch.zeros((1, 3, 4), dtype=torch.int32), i32, i32, table, table)]
+    for n, call_ in enumerate(bad):
+        with pytest.raises(ValueError) as e:
+            call_()
+        assert "current CUDA device" not in str(e.value), n
+    one = torch.zeros((3, 1, 640), dtype=torch.bfloat16)[..., :128].unflatten(-1, (2, 64))
+    assert tm._token_rows(one, "q") == 640      # a one-token slice of a packed projection
+    assert tm._token_rows(x, "q") == 128
+    with pytest.raises(ValueError, match="follow each other"):
+        tm._token_rows(torch.zeros((2, 8, 2, 64), dtype=torch.bfloat16)[:, :4], "q")

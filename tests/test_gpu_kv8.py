@@ -193,7 +193,6 @@ def test_append_index_strides_and_missing_pages():
                       for _ in range(B)])
     index[0, 1, 5], index[1, 0, 0], index[2, 1, 39] = -1, n_src, 2 ** 31 - 1
     check_append(cache, k, v, [0, 10, 20], [40, 31, 17], index, n=40)
-    assert torch.equal(packed, packed)
 
 
 @pytest.mark.parametrize("fmt", [ref.INT8, ref.E4M3])
@@ -329,6 +328,88 @@ def test_attention_of_rows_that_do_not_see_a_nan(fmt):
     clean = Cache(41, 2, 1, 64, 16, fmt, 3)
     want = clean.attend(q, ints([33, 19]))
     assert torch.equal(got[0, :2], want[0, :2]) and torch.equal(got[1], want[1])
+
+
+def test_attention_of_rows_that_do_not_see_an_infinity():
+    """An infinite range reads as NaN to the rows that see its block and not at all to others."""
+    import torch
+    for fmt in (ref.INT8, ref.E4M3):
+        cache = Cache(41, 1, 1, 64, 16, fmt, 3)
+        q, last = rand((1, 3, 4, 64), 42), int(cache.table[0, 2])
+        want = cache.attend(q, ints([33]))
+        cache.vr[last] = float("inf")
+        got = cache.attend(q, ints([33]))
+        assert torch.equal(got[0, :2], want[0, :2]) and torch.isnan(got[0, 2]).all()
+
+
+def test_attention_with_a_far_larger_range_that_weighs_nothing():
+    """Keys of weight 2^-40 and less whose values are 2^20 times the others' (and the other way
+    round, and ranges that fall by 2^60 a page): the others keep the precision they would have
+    alone. Bound: 2^-8 of o for bf16, 2^-10 of the weighted |v| for P (2^-11) and the scores."""
+    import torch
+    H, D, page, mp = 1, 128, 16, 8
+    for fmt in (ref.INT8, ref.E4M3):
+        for big in ([0], [7], [3], [0, 2, 4, 6]):
+            cache = Cache(60, 1, H, D, page, fmt, mp)
+            q = rand((1, 1, 4, D), 61).abs()
+            # |q| only, and keys that are all of one sign: theirs are far below the others' scores
+            signs = cache.k8.float().abs().clamp(min=1)
+            cache.k8.copy_(signs.to(cache.k8.dtype))
+            for j in big:
+                pg = int(cache.table[0, j])
+                cache.k8[pg] = (-signs[pg]).to(cache.k8.dtype)
+                cache.vr[pg] *= 2.0 ** 20
+            kc, vc, kr, vr = cache.image()
+            tab = cache.table.cpu().numpy()
+            k, _ = ref.values(kc, kr, tab, 0, 0, mp * page, fmt)
+            v, _ = ref.values(vc, vr, tab, 0, 0, mp * page, fmt)
+            scale = 8.0 / math.sqrt(D)
+            got = cache.attend(q, ints([mp * page]), scale=scale).double().cpu().numpy()
+            for g in range(4):
+                sc = k @ q[0, 0, g].double().cpu().numpy() * scale
+                p = np.exp(sc - sc.max())
+                p /= p.sum()
+                rows = np.repeat([j in big for j in range(mp)], page)
+                assert p[rows].max() < 2.0 ** -60
+                err = np.abs(got[0, 0, g] - p @ v)
+                assert (err <= np.abs(p @ v) * 2.0 ** -8 + (p @ np.abs(v)) * 2.0 ** -10).all()
+    cache = Cache(62, 1, H, D, page, ref.INT8, mp)
+    cache.vr[cache.table[0].long(), 0] = 2.0 ** torch.tensor([50.0, 40, -20, -80, -100, 0, 50, -40],
+                                                             device="cuda")
+    check_attention(cache, rand((1, 1, 4, D), 63), [mp * page])
+
+
+def test_torch_conveniences_make_the_same_calls():
+    import torch
+    B, H, Hq, D, page, mp = 2, 2, 8, 64, 16, 4
+    a = Cache(70, B, H, D, page, ref.E4M3, mp, extra=8)
+    b = Cache(70, B, H, D, page, ref.E4M3, mp, extra=8)
+    c = tm.Kv8Cache(b.k8, b.v8, b.kr, b.vr)
+    packed = rand((B, 9, (Hq + 2 * H) * D), 71)
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in packed.split([Hq * D, H * D, H * D], -1))
+    f = torch.from_numpy(tm.tm_rope_inv_freq(D, 10000.0)).cuda()
+    qo, ko = tm.rope(q, k, f, first=3)
+    in_place = packed.clone()
+    q2, k2 = (t.unflatten(-1, (-1, D)) for t in in_place.split([Hq * D, H * D, H * D], -1)[:2])
+    tm.rope(q2, k2, f, first=3, out=(q2, k2))
+    assert torch.equal(q2, qo) and torch.equal(k2, ko)
+    lens = ints([5, 11])
+    a.append(ko, v, lens, strides=(H * D, (Hq + 2 * H) * D))
+    tm.kv8_append(c, ko, v, lens, b.table)
+    assert torch.equal(a.k8.view(torch.int8), b.k8.view(torch.int8)) and torch.equal(a.vr, b.vr)
+    lens = lens + 9
+    w = torch.zeros((B, H, mp * page), device="cuda")
+    w2 = torch.zeros_like(w)
+    o = a.attend(qo, lens, w)
+    assert torch.equal(tm.kv8_attention(c, qo, lens, b.table, weights=w2), o)
+    assert torch.equal(w, w2)
+    index, kept = tm.kv_select(w, 6, 1, 2, lens)
+    new = b.unused[:B].view(B, 1).cuda()
+    nw = torch.zeros((B, H, 6), device="cuda")
+    tm.kv8_compact(c, index, kept, lens, b.table, new, w, nw)
+    assert torch.equal(nw, w.gather(2, index.long()))
+    wk = tm.key_weights(qo, ko, 4)
+    np.testing.assert_allclose(wk.sum(-1).cpu().numpy(), 4 * Hq / H, rtol=1e-4)
 
 
 def test_attention_accumulates_weights_and_repeats_to_the_bit():
