@@ -181,6 +181,49 @@ def test_select_many_rows_on_several_streams():
         np.testing.assert_array_equal(o.cpu().numpy(), want)
 
 
+def test_positions_selection_and_compact_captured():
+    """One graph of rotary positions, selection and compact, replayed on new inputs and lengths,
+    against the calls themselves."""
+    import torch
+    B, H, D, page, mp, keep = 2, 2, 64, 16, 8, 24
+    c = tm.Kv8Cache.empty(40, H, page, D)
+    g = torch.Generator().manual_seed(3)
+    c.k8.copy_(torch.randint(-127, 128, c.k8.shape, generator=g).to(torch.int8))
+    c.v8.copy_(torch.randint(-127, 128, c.v8.shape, generator=g).to(torch.int8))
+    c.k_range.copy_(torch.rand(40, H, generator=g).to(torch.bfloat16).float() + 1)
+    c.v_range.copy_(torch.rand(40, H, generator=g).to(torch.bfloat16).float() + 1)
+    pages = torch.randperm(40, generator=g).to(torch.int32)
+    table, to = pages[:16].view(B, mp).cuda(), pages[16:20].view(B, 2).cuda()
+    w, lens = torch.rand((B, H, 128), device="cuda"), ints([128, 60])
+    index, kept = (torch.empty(s, dtype=torch.int32, device="cuda") for s in ((B, H, keep), (B,)))
+    nw = torch.zeros((B, H, keep), device="cuda")
+    q, f = rand((B, 5, 4, D), 92), torch.from_numpy(tm.tm_rope_inv_freq(D, 10000.0)).cuda()
+    pos, out = ints(np.arange(10).reshape(2, 5)), torch.empty_like(q)
+
+    def step():
+        tm.rope(q, None, f, pos, out=(out, None))
+        tm.tm_kv_select(w, 128, lens, B, H, 128, keep, 2, 5, index, kept)
+        tm.kv8_compact(c, index, kept, lens, table, to, w, nw)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n, seed in (([128, 60], 1), ([17, 128], 2), ([0, 5], 3)):
+        w.copy_(torch.rand(w.shape, generator=torch.Generator().manual_seed(seed)))
+        lens.copy_(ints(n))
+        q.copy_(rand(q.shape, 100 + seed))
+        pos.copy_(pos * 3 + seed)
+        graph.replay()
+        got = [t.clone() for t in (out, index, kept, c.k8, c.v8, c.k_range, c.v_range, nw)]
+        for t in (out, index, kept):
+            t.fill_(-7)
+        step()
+        for a, b in zip(got, (out, index, kept, c.k8, c.v8, c.k_range, c.v_range, nw)):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("fmt", [ref.INT8, ref.E4M3])

@@ -537,3 +537,40 @@ def test_work_on_another_stream_is_ordered_by_it():
     cache.attend(q, lens, o=got2, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(got2, want)
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    """Attention, append and weights on two streams that overlap, against one after the other."""
+    import torch
+    caches = [Cache(80 + i, 3, 2, 128, 32, fmt, 40) for i, fmt in enumerate((ref.INT8, ref.E4M3))]
+    qs = [rand((3, 2, 8, 128), 82 + i) for i in range(2)]
+    lens = [ints([1280, 700, 3]), ints([900, 1279, 0])]
+    w = [torch.zeros((3, 2, 1280), device="cuda") for _ in range(4)]
+    want = [c.attend(q, n, x) for c, q, n, x in zip(caches, qs, lens, w)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for rep in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(caches[i].attend(qs[i], lens[i], w[2 + i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+        assert torch.equal(w[i], w[2 + i])
+
+
+def test_sequences_that_share_pages_and_a_large_batch():
+    """Pages read by several sequences; a batch of more sequences than a block has threads."""
+    cache = Cache(84, 2, 1, 64, 16, ref.INT8, 4)
+    cache.table[1, :2] = cache.table[0, :2]
+    check_attention(cache, rand((2, 1, 4, 64), 85), [64, 50], True)
+    rng = np.random.default_rng(86)
+    big = Cache(87, 1100, 1, 64, 16, ref.E4M3, 1)
+    check_attention(big, rand((1100, 1, 1, 64), 88), rng.integers(0, 17, 1100).tolist(), True)
+
+
+def test_many_rows_take_several_tiles():
+    """33 rows a kv head: three row tiles, the last one partly filled; and one query of 40 heads."""
+    cache = Cache(89, 2, 1, 64, 32, ref.INT8, 3)
+    check_attention(cache, rand((2, 11, 3, 64), 90), [96, 7], True)
+    check_attention(cache, rand((2, 1, 40, 64), 91), [96, 33], True)
