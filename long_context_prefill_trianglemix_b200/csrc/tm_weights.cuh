@@ -17,15 +17,18 @@
 // CTA (576 threads, one per SM, persistent): warps 0-15 are four reduction
 // warpgroups, each with a 128-column S buffer in TMEM; warp 16 loads by TMA; warp
 // 17 issues the MMAs. With four A tiles an item each warpgroup has one; with fewer
-// the warpgroups of a tile take its B tiles in turn (phases). A warpgroup takes its scores to registers in
-// halves, so the next MMA into its buffer runs while it reduces the second half
-// and the other warpgroups work. A q tile packs floor(128 / G) tokens of all G q
-// heads of the group, so short L wastes no rows.
+// the warpgroups of a tile take its B tiles in turn (phases). A warpgroup takes its
+// scores to registers in halves, so the next MMA into its buffer runs while it
+// reduces the second half and the other warpgroups work. A q tile packs
+// floor(128 / G) tokens of all G q heads of the group, so short L wastes no rows.
 //
 // Bound: one exponential per score and pass. At 16 MUFU results a clock and SM a
-// 128 x 128 tile takes 1024 clocks, twice its MMA time, so 3 of 8 exponentials
+// 128 x 128 tile takes 1024 clocks, twice its MMA time, so 2 of 8 exponentials
 // run on the FMA pipe (ex2x2_quintic). Four warpgroups rather than two hide the
-// dependent-issue latency of the reductions.
+// dependent-issue latency of the reductions. Measured: 131072 keys, the last 256
+// queries, 32 q and 8 kv heads, D = 128: 545 us (2 x 275 GFLOP, 1.0 PFLOP/s; 1.07 G
+// exponentials a pass, 231 us of MUFU alone at 1965 MHz), 650 us under the power
+// cap of a long run.
 
 constexpr int kWtTiles = 4;  // A tiles, reduction warpgroups
 constexpr int kWtThreads = 128 * kWtTiles + 64;
@@ -82,13 +85,10 @@ __device__ __forceinline__ F2 ex2x2_quintic(const Quintic& k, F2 x) {
                        __float_as_uint(tb) * 8388608u + 0x3F800000u));
 }
 
-// kWtPoly of every 8 pairs go to the FMA pipe, the others to MUFU.
-#ifndef WT_POLY
-#define WT_POLY 2
-#endif
-constexpr int kWtPoly = WT_POLY;
+// Two of every 8 pairs go to the FMA pipe, the others to MUFU. The 131072-key case
+// with 0, 1, 2, 3 and 4 of them: 625, 575, 560, 576-595 and 627-654 us.
 __device__ __forceinline__ F2 wt_exp_pair(const Quintic& k, int e, F2 x) {
-  constexpr uint32_t kMask = kWtPoly == 0 ? 0u : kWtPoly == 1 ? 0x08u : kWtPoly == 2 ? 0x22u : kWtPoly == 3 ? 0x4Au : 0xAAu;
+  constexpr uint32_t kMask = 0x22u;
   if ((kMask >> ((e >> 1) & 7)) & 1u) return ex2x2_quintic(k, x);
   float a, b;
   unpack2(x, a, b);
