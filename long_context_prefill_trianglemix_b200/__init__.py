@@ -10,8 +10,10 @@ If the library has not been built, every call raises; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
+import operator
 import os
 from typing import Any, NamedTuple
 
@@ -382,7 +384,7 @@ def _device_ptrs(*xs):
         try:
             device = x.get_device()  # -1: the host
         except AttributeError:
-            out.append(int(x))
+            out.append(operator.index(x))  # an address; not a number that an array holds
             continue
         if device != here:
             if here is not None or device < 0 or device != (_device or _find_current_stream())():
@@ -522,7 +524,29 @@ def trianglemix_attention(q, k, v, S, W, L, layer, tri_start, scale=None, out=No
 
 
 # The operators around the attention, on torch tensors. Token counts and tables are int32 CUDA
-# tensors, k and v bf16; shapes and types are checked here, ranges of values on the device.
+# tensors, k and v bf16; shapes and types are checked here, ranges of values on the device. With a
+# `stream`, results and workspaces that a call allocates belong to that stream.
+
+def _on(stream):
+    """A context in which torch allocates and fills on ``stream`` (None: the current one): a
+    workspace given back at the end of a call is then reused behind the call's kernels, and a
+    result's zeros are there before them."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _workspace(workspace, size, device, stream):
+    import torch
+    if workspace is not None:
+        return _need(workspace, "workspace", torch.uint8, None)
+    with _on(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
 
 def _need(x, name, dtype, *shape):
     """x has this dtype and shape (None: any size) and is contiguous."""
@@ -565,8 +589,12 @@ def rope(q, k, inv_freq, positions=None, first=0, rot=None, interleaved=False, m
     _need(inv_freq, "inv_freq", torch.float64, rot // 2)
     if positions is not None:
         _need(positions, "positions", torch.int32, B, N)
-    outs = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-            for t in (q, k)] if out is None else list(out)
+    if out is None:
+        with _on(stream):
+            outs = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                    for t in (q, k)]
+    else:
+        outs = list(out)
     H, st = [], []
     for t, o, name in ((q, outs[0], "q"), (k, outs[1], "k")):
         if t is None:
@@ -644,14 +672,15 @@ def kv8_attention(cache, q, lens, table, scale=None, weights=None, accumulate=Fa
     mp = _need(table, "table", torch.int32, B, None).shape[1]
     if weights is not None:
         _need(weights, "weights", torch.float32, B, H, None)
-    o = _need(_out(q, out), "out", torch.bfloat16, B, nq, Hq, D)
+    with _on(stream):
+        o = _out(q, out)
+    _need(o, "out", torch.bfloat16, B, nq, Hq, D)
     size = tm_kv8_attn_workspace_size(B, nq, Hq, H, D, mp, page, weights is not None)
-    if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    workspace = _workspace(workspace, size, q.device, stream)
     tm_kv8_attn_fwd(q, o, B, nq, Hq, H, D, 1.0 / math.sqrt(D) if scale is None else scale,
                     *cache._args(), table, mp, lens, weights,
                     0 if weights is None else weights.shape[2], accumulate, workspace,
-                    workspace.numel() * workspace.element_size(), stream)
+                    workspace.numel(), stream)
     return o
 
 
@@ -666,14 +695,14 @@ def key_weights(q, k, L, lens=None, scale=None, weights=None, accumulate=False, 
     if lens is not None:
         _need(lens, "lens", torch.int32, B)
     if weights is None:
-        weights = torch.zeros((B, Hkv, N), device=q.device)
+        with _on(stream):
+            weights = torch.zeros((B, Hkv, N), device=q.device)
     _need(weights, "weights", torch.float32, B, Hkv, None)
     size = tm_key_weights_workspace_size(B, Hq, Hkv, N, D, L)
-    if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    workspace = _workspace(workspace, size, q.device, stream)
     tm_key_weights_fwd(q, k, B, Hq, Hkv, N, D, 1.0 / math.sqrt(D) if scale is None else scale, L,
                        lens, weights, weights.shape[2], accumulate, workspace,
-                       workspace.numel() * workspace.element_size(), stream)
+                       workspace.numel(), stream)
     return weights
 
 
@@ -684,8 +713,9 @@ def kv_select(weights, keep, sinks=0, recent=0, lens=None, n=None, stream=None):
     B, H, cap = _need(weights, "weights", torch.float32, None, None, None).shape
     if lens is not None:
         _need(lens, "lens", torch.int32, B)
-    index = torch.empty((B, H, keep), dtype=torch.int32, device=weights.device)
-    kept = torch.empty(B, dtype=torch.int32, device=weights.device)
+    with _on(stream):
+        index = torch.empty((B, H, keep), dtype=torch.int32, device=weights.device)
+        kept = torch.empty(B, dtype=torch.int32, device=weights.device)
     tm_kv_select(weights, cap, lens, B, H, cap if n is None else n, keep, sinks, recent, index, kept,
                  stream)
     return index, kept

@@ -247,3 +247,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     assert tm._token_rows(x, "q") == 128
     with pytest.raises(ValueError, match="follow each other"):
         tm._token_rows(torch.zeros((2, 8, 2, 64), dtype=torch.bfloat16)[:, :4], "q")
+
+
+def test_binding_takes_addresses_not_the_numbers_of_an_array():
+    """A host array of one number is not the address it holds, nor is a float one."""
+    for x in (np.array([4096], np.int32), np.array([4096.0], np.float32), 4096.0):
+        with pytest.raises(TypeError):
+            tm.tm_kv_select(A, 8, x, 1, 1, 8, 4, 0, 0, A)
+        with pytest.raises(TypeError):
+            tm.tm_kv8_attn_fwd(A, A, 1, 1, 1, 1, 64, 1.0, A, A, A, A, 1, 16, 0, x, 1, A, None, 0, 0,
+                               A, 1 << 30)

@@ -311,3 +311,47 @@ def test_a_prompt_and_its_decode_with_eviction(fmt):
     for step in range(20, 24):
         lens = decode(step, new_table, lens, new_acc)
     assert lens.tolist() == [smaller + 4] * B
+
+
+def test_conveniences_allocate_on_the_stream_they_run_on():
+    """With the current stream busy: a result's zeros come before its kernel, a workspace that
+    is given back is not overwritten from the current stream."""
+    import torch
+    B, N, Hq, H, D, L = 2, 300, 8, 2, 64, 40
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn((B, N, h, D), generator=g, device="cuda").to(torch.bfloat16)
+               for h in (Hq, H, H))
+    f = torch.from_numpy(tm.tm_rope_inv_freq(D, 1e4)).cuda()
+    lens = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    full = torch.tensor([300, 77], dtype=torch.int32, device="cuda")
+    table = torch.arange(2 * 5, dtype=torch.int32, device="cuda").view(2, 5)
+    cache = tm.Kv8Cache.empty(10, H, 64, D)
+
+    def steps(stream):
+        qr, kr = tm.rope(q, k, f, stream=stream)
+        tm.kv8_append(cache, kr, v, lens, table, counts=full, stream=stream)
+        w = tm.key_weights(qr, kr, L, lens=full, stream=stream)
+        o = tm.kv8_attention(cache, q[:, -1:].contiguous(), full, table, stream=stream)
+        index, kept = tm.kv_select(w, 50, 2, 8, lens=full, stream=stream)
+        return qr, kr, w, o, index, kept
+
+    want = steps(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)
+        ws = tm.tm_key_weights_workspace_size(B, Hq, H, N, D, L)
+        with torch.cuda.stream(side):
+            last = q[:, -1:].contiguous()
+        got = [tm.key_weights(q, k, L, lens=full, stream=stream)]
+        fill = torch.full((ws,), 255, dtype=torch.uint8, device="cuda")
+        o = tm.kv8_attention(cache, last, full, table, stream=stream)
+        got += [o, *tm.kv_select(want[2], 50, 2, 8, lens=full, stream=stream)]
+        torch.cuda.synchronize()
+        plain = tm.key_weights(q, k, L, lens=full)
+        assert torch.equal(got[0], plain) and torch.equal(got[1], want[3])
+        assert torch.equal(got[2], want[4]) and torch.equal(got[3], want[5])
+        assert int(fill.min()) == 255
+    turned = tm.rope(q, k, f, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(turned[0], want[0]) and torch.equal(turned[1], want[1])
