@@ -1291,7 +1291,7 @@ struct DeviceInfo {
   std::atomic<bool> attr_set[2] = {false, false};
   std::atomic<bool> probe_attr_set[2] = {false, false};
   std::atomic<bool> disc_attr_set[2] = {false, false};
-  std::atomic<bool> weights_attr_set[4] = {false, false, false, false};
+  std::atomic<bool> weights_attr_set[6] = {};
   std::atomic<bool> kv8_attr_set[16] = {};
 };
 
@@ -1731,6 +1731,8 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
   if (int rc = set_smem_once(di->weights_attr_set[kidx], weights_kernel<D, 1>, C::kSmem)) return rc;
   if (int rc = set_smem_once(di->weights_attr_set[2 + kidx], weights_kernel<D, 2>, C::kSmem))
     return rc;
+  if (int rc = set_smem_once(di->weights_attr_set[4 + kidx], weights_kernel<D, 2, true>, C::kSmem))
+    return rc;
   const WtLayout l = weights_layout(a.B, a.Hq, a.Hkv, a.N, a.L);
   if (a.ws_bytes < l.total) return TM_ERR_INVALID_ARG;
   WtParams p;
@@ -1765,15 +1767,23 @@ int launch_key_weights_d(const KeyWeightsArgs& a, DeviceInfo* di) {
                    st, 1, tq, tk, p))
     return TM_ERR_CUDA;
   const long long rows = bg * l.nqt * 128;
-  if (launch_early(weights_lse_kernel, dim3(static_cast<unsigned>(rows / 32)), 256, 0, st, 1, p))
+  int one = 1, group = 1;
+  weights_shape(bg, l.nkt, l.nqt, false, &group, &one);
+  const long long items = bg * ((l.nkt + group - 1) / group);
+  // Where a CTA of pass 2 has one item, it joins pass 1's parts itself (in so few steps of its
+  // 512 threads, eight loads each) and a launch is saved: 8 heads of 300 keys 13.5 -> 12.2 us,
+  // 64 of 1000 keys 57.2 -> 51.5; several items a CTA join again for every head that they
+  // meet: 8 heads of 20000 keys 45 -> 52, of 131072 keys 114 -> 150.
+  const bool join = l.nqt <= kWtLse && items <= sms &&
+                    (l.nqt + kWtTiles - 1) / kWtTiles * ((p.parts + 7) / 8) <= 4;
+  if (!join && launch_early(weights_lse_kernel, dim3(static_cast<unsigned>(rows / 32)), 256, 0, st, 1, p))
     return TM_ERR_CUDA;
-  int one = 1;
-  weights_shape(bg, l.nkt, l.nqt, false, &p.group, &one);
-  p.items = static_cast<int>(bg * ((l.nkt + p.group - 1) / p.group));
-  if (launch_early(weights_kernel<D, 2>, dim3(std::min<unsigned>(p.items, sms)), kWtThreads, C::kSmem,
-                   st, 1, tq, tk, p))
+  p.group = group;
+  p.items = static_cast<int>(items);
+  if (launch_early(join ? weights_kernel<D, 2, true> : weights_kernel<D, 2>,
+                   dim3(std::min<unsigned>(p.items, sms)), kWtThreads, C::kSmem, st, 1, tq, tk, p))
     return TM_ERR_CUDA;
-  return counted(3);
+  return counted(join ? 2 : 3);
 }
 
 }  // namespace

@@ -136,6 +136,7 @@ struct WtBars {
   uint64_t s_full[kWtTiles], s_empty[kWtTiles];
   uint64_t l_full[kWtLse], l_empty[kWtLse];
   uint64_t x_full[2], x_empty[2];  // [A tile]: the sums above
+  uint64_t j_full, j_empty;        // a kv head's joined statistics
   uint64_t mma_done;
   uint32_t tmem;
   int abort_flag;
@@ -190,7 +191,36 @@ __device__ __forceinline__ bool wt_item(const WtParams& p, int i, WtItem& it) {
   return true;
 }
 
-template <int D, int PASS>
+// Joins parts j, j + step, ... of a row's statistics (`per` apart), F loads at a time.
+template <int F>
+__device__ __forceinline__ void wt_join(const WtParams& p, const float2* s, long long per, int j,
+                                        int step, float& m, float& l) {
+  m = -1.7e38f;
+  l = 0.f;
+  for (int k0 = j; k0 < p.parts; k0 += F * step) {
+    float2 v[F];
+#pragma unroll
+    for (int u = 0; u < F; ++u)
+      v[u] = k0 + step * u < p.parts ? s[(k0 + step * u) * per] : make_float2(-1.7e38f, 0.f);
+#pragma unroll
+    for (int u = 0; u < F; ++u) {
+      const float mn = fmax3_nan(m, v[u].x, v[u].x);
+      l = l * ex2(m - mn) + v[u].y * ex2(v[u].x - mn);
+      m = mn;
+    }
+  }
+}
+
+// Whether row x of the q tiles of a sequence of len tokens is one.
+__device__ __forceinline__ bool wt_there(const WtParams& p, int len, int x) {
+  const int c = x & 127;
+  return c < p.tpt * p.G && (x >> 7) * p.tpt + c / p.G < imin(p.L, len);
+}
+
+// JOIN (pass 2): the statistics of a kv head's rows are joined from pass 1's parts by
+// the reducing warps, into the memory of the lse slots; at most kWtLse q tiles. Without
+// it weights_lse_kernel does so in between.
+template <int D, int PASS, bool JOIN = false>
 __global__ void __launch_bounds__(kWtThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ WtParams p) {
@@ -227,6 +257,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       mbar_init(&bars->x_full[i], 4 * (kWtTiles / p.group > 1 ? kWtTiles / p.group - 1 : 1));
       mbar_init(&bars->x_empty[i], 4);
     }
+    mbar_init(&bars->j_full, 4 * kWtTiles);
+    mbar_init(&bars->j_empty, 4 * kWtTiles);
     mbar_init(&bars->mma_done, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -285,6 +317,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             load_k(sB + st * C::kTile, &bars->b_full[st], it, t);
           } else {
             load_q(sB + st * C::kTile, &bars->b_full[st], it, t);
+            if (JOIN) {
+              ++bc;
+              continue;
+            }
             const int ls = bc % kWtLse;
             if (!(ok = wait_bar(&bars->l_empty[ls], ((bc / kWtLse) & 1) ^ 1, abort_flag,
                                 kSiteWeights))) {
@@ -306,7 +342,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       for (uint32_t i = 0; i < kWtStages; ++i)
         if (bc > i) drain_wait(&bars->b_full[i], ((bc - 1 - i) / kWtStages) & 1);
       for (uint32_t i = 0; i < kWtLse; ++i)
-        if (PASS == 2 && bc > i) drain_wait(&bars->l_full[i], ((bc - 1 - i) / kWtLse) & 1);
+        if (PASS == 2 && !JOIN && bc > i) drain_wait(&bars->l_full[i], ((bc - 1 - i) / kWtLse) & 1);
     }
   } else if (warp == 4 * kWtTiles + 1) {
     const bool leader = elect_one();
@@ -352,10 +388,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const Quintic kq = quintic();
     const F2 sl2 = both(p.sl2);
     uint32_t bc = 0, sc = 0, xc = 0;  // B tiles of the CTA, scores and items of this warpgroup
+    uint32_t jc = 0;  // kv heads joined, and the last of them
+    int joined = -1;
     const int phases = kWtTiles / p.group, ai = wg & (p.group - 1), phase = wg / p.group;
     bool ok = true;
     // another's B tile: only let its lse slot go
     auto pass_over = [&](uint32_t n) {
+      if (JOIN) return true;
       const int ls = n % kWtLse;
       const bool here = __all_sync(
           0xffffffffu, wait_bar(&bars->l_full[ls], (n / kWtLse) & 1, abort_flag, kSiteWeights));
@@ -365,6 +404,30 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
       WtItem it;
       if (!wt_item<PASS>(p, i, it)) continue;
+      if (PASS == 2 && JOIN && it.b * p.Hkv + it.g != joined) {
+        // This kv head's statistics, in place of the slots: all 16 warps have left the head
+        // before, and each joins some rows of this one.
+        if (joined >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->j_empty);
+          ok = __all_sync(0xffffffffu, wait_bar(&bars->j_empty, (jc & 1) ^ 1, abort_flag, kSiteWeights));
+          if (!ok) break;
+        }
+        joined = it.b * p.Hkv + it.g;
+        const long long per = static_cast<long long>(p.nqt) * 128;
+        const float2* st = p.stats + static_cast<long long>(joined) * p.parts * per;
+        float* table = reinterpret_cast<float*>(smem + C::kLse);
+        for (int x = tid; x < p.nqt * 128; x += 128 * kWtTiles) {
+          float m, l;
+          wt_join<8>(p, st + x, per, 0, 1, m, l);
+          table[x] = wt_there(p, it.len, x) ? -(m + log2f(l)) : -INFINITY;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->j_full);
+        ok = __all_sync(0xffffffffu, wait_bar(&bars->j_full, jc & 1, abort_flag, kSiteWeights));
+        if (!ok) break;
+        ++jc;
+      }
       if (ai >= it.na) {  // no A tile for this warpgroup
         for (int t = it.t0; PASS == 2 && t < it.t1 && ok; ++t, ++bc) ok = pass_over(bc);
         continue;
@@ -385,7 +448,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         const int ls = bc % kWtLse;
         bool here = wait_bar(&bars->s_full[wg], sc & 1, abort_flag, kSiteWeights);
-        if (PASS == 2)
+        if (PASS == 2 && !JOIN)
           here = here && wait_bar(&bars->l_full[ls], (bc / kWtLse) & 1, abort_flag, kSiteWeights);
         if (!(ok = __all_sync(0xffffffffu, here))) break;
         ++sc;
@@ -399,7 +462,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           c_hi = imin(p.tpt, rows - t * p.tpt) * p.G;
         }
         const bool full = __all_sync(0xffffffffu, !live || (c_lo == 0 && c_hi == 128));
-        const ulonglong2* z = reinterpret_cast<const ulonglong2*>(smem + C::kLse + ls * 512);
+        const ulonglong2* z =
+            reinterpret_cast<const ulonglong2*>(smem + C::kLse + (JOIN ? t : ls) * 512);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t s[2][32];
@@ -476,7 +540,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           unpack2(add2(acc0, acc1), r0, r1);
           sum += r0 + r1 + a0;
         }
-        if (PASS == 2) {
+        if (PASS == 2 && !JOIN) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->l_empty[ls]);
         }
@@ -529,20 +593,8 @@ __global__ void __launch_bounds__(256) weights_lse_kernel(const WtParams p) {
   const long long per = static_cast<long long>(p.nqt) * 128;
   const int x = threadIdx.x & 31, j = threadIdx.x >> 5;
   const long long i = blockIdx.x * 32LL + x, bg = i / per, r = i - bg * per;
-  const float2* s = p.stats + bg * p.parts * per + r;
-  float m = -1.7e38f, l = 0.f;
-  for (int k0 = j; k0 < p.parts; k0 += 32) {
-    float2 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      v[u] = k0 + 8 * u < p.parts ? s[(k0 + 8 * u) * per] : make_float2(-1.7e38f, 0.f);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float mn = fmax3_nan(m, v[u].x, v[u].x);
-      l = l * ex2(m - mn) + v[u].y * ex2(v[u].x - mn);
-      m = mn;
-    }
-  }
+  float m, l;
+  wt_join<4>(p, p.stats + bg * p.parts * per + r, per, j, 8, m, l);
   s_part[j][x] = make_float2(m, l);
   __syncthreads();
   if (j) return;
@@ -552,8 +604,7 @@ __global__ void __launch_bounds__(256) weights_lse_kernel(const WtParams p) {
     l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
     m = mn;
   }
-  const int rows = imin(p.L, wt_len(p, static_cast<int>(bg / p.Hkv)));
-  const int c = static_cast<int>(r & 127);
-  const bool there = c < p.tpt * p.G && (r >> 7) * p.tpt + c / p.G < rows;
-  p.nlse[i] = there ? -(m + log2f(l)) : -INFINITY;
+  p.nlse[i] = wt_there(p, wt_len(p, static_cast<int>(bg / p.Hkv)), static_cast<int>(r))
+                  ? -(m + log2f(l))
+                  : -INFINITY;
 }
