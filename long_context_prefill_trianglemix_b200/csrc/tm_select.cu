@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectAr
   constexpr int kRun = 32 * KPL;  // weights of a warp in a round
   __shared__ __align__(16) int hist[3][kBins];
   __shared__ int coarse[3][32];       // sums of 64 bins
-  __shared__ int s_pick[2];           // chosen bin, kept tokens above it
+  __shared__ int s_pick[3][3];        // of a pass: chosen bin, its tokens, kept tokens above it
   __shared__ int s_gt[32], s_eq[32];  // per warp: tokens above T, equal to T
   __shared__ int s_count[2];          // the same of this CTA
   cg::cluster_group cluster = cg::this_cluster();
@@ -163,14 +163,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectAr
       const int in = 31 - __clz(__ballot_sync(0xffffffffu, upto >= need));
       if (lane == in) {
         const bool hi_bin = upto - f.x >= need;  // bins above, and the lane's upper one
-        s_pick[0] = 64 * top + 2 * lane + hi_bin;
-        s_pick[1] = hi_bin ? upto - f.x - f.y : upto - f.x;
+        s_pick[pass][0] = 64 * top + 2 * lane + hi_bin;
+        s_pick[pass][1] = hi_bin ? f.y : f.x;
+        s_pick[pass][2] = hi_bin ? upto - f.x - f.y : upto - f.x;
       }
     }
     __syncthreads();
-    prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
-    need -= s_pick[1];
-    __syncthreads();  // s_pick has been read
+    prefix |= static_cast<uint32_t>(s_pick[pass][0]) << shift;
+    need -= s_pick[pass][2];
+    // The whole bin is kept (usual once it is down to a token or two): every key from its
+    // lowest on. Key 0 is no weight, so a bin that starts there is looked into.
+    if (pass < 2 && need == s_pick[pass][1] && prefix != 0) {
+      --prefix;
+      need = 0;
+      break;
+    }
   }
   // prefix is T; `need` tokens equal to it are kept, the first ones of the row.
   auto count = [&](int& gt, int& eq) {
