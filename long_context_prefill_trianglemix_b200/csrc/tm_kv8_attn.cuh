@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
 
   // Lane i & 31 holds where unit i lies; the next 32 are looked up a batch ahead.
   UnitAt cur = locate<D, UT>(p, pre, xs + lane, xe), nxt = cur;
+  const uint64_t policy = evict_first();  // leaves L2 to the scores
   auto issue = [&](int i, int batch) {
     if (i >= n_units || lane != (i & 31)) return;
     const int row = (i >> 5) == batch ? cur.row : nxt.row;
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       return;
     }
     mbar_arrive_expect_tx(bar, 2 * C::kHalf);
-    tma_load_2d(ring_addr + st * 2 * C::kHalf, &tk, bar, 0, row);
-    tma_load_2d(ring_addr + st * 2 * C::kHalf + C::kHalf, &tv, bar, 0, row);
+    tma_load_2d(ring_addr + st * 2 * C::kHalf, &tk, bar, 0, row, policy);
+    tma_load_2d(ring_addr + st * 2 * C::kHalf + C::kHalf, &tv, bar, 0, row, policy);
   };
   for (int i = 0; i < S - 1; ++i) issue(i, 0);
   load_ranges<D>(p, cur);
@@ -831,28 +832,43 @@ __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
       make_uint2(sm100::pack_bf16x2(o.x * inv, o.y * inv), sm100::pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-// The weight of each key: sum over the kv head's rows of 2^(s - lse).
+// The weight of each key: sum over the kv head's rows of 2^(s - lse). A CTA takes runs
+// of 1024 keys, four a thread with their loads together.
+constexpr int kKeys = 4, kKeyRun = 256 * kKeys;
 template <int NT>
 __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
   pdl_launch();
   pdl_wait();
   const int bh = blockIdx.y, b = bh / p.a.c.Hkv, h = bh - b * p.a.c.Hkv;
   const long long len = min(static_cast<long long>(clamp_len(p, b)), p.a.weights_stride);
-  for (long long j = blockIdx.x * 256LL + threadIdx.x; j < len; j += gridDim.x * 256LL) {
-    float w = 0.f;
+  for (long long j0 = static_cast<long long>(blockIdx.x) * kKeyRun + threadIdx.x; j0 < len;
+       j0 += static_cast<long long>(gridDim.x) * kKeyRun) {
+    float w[kKeys] = {};
     for (int rt = 0; rt < p.RT; ++rt) {
       const long long item = static_cast<long long>(b) * p.items_per_b + h * p.RT + rt;
-      const float4* s = reinterpret_cast<const float4*>(p.scores + (item * p.cap + j) * p.rs);
       const float4* z = reinterpret_cast<const float4*>(p.lse + item * (8 * NT));
+      const float4* s[kKeys];  // (a key past the end reads the last one's)
+#pragma unroll
+      for (int u = 0; u < kKeys; ++u)
+        s[u] = reinterpret_cast<const float4*>(p.scores + (item * p.cap + min(j0 + 256 * u, len - 1)) * p.rs);
 #pragma unroll
       for (int n = 0; n < 2 * NT; ++n) {
         if (4 * n >= p.rs) break;
-        const float4 x = s[n], y = z[n];
-        w += (ex2(x.x - y.x) + ex2(x.y - y.y)) + (ex2(x.z - y.z) + ex2(x.w - y.w));
+        const float4 y = z[n];
+        float4 x[kKeys];
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) x[u] = s[u][n];
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u)
+          w[u] += (ex2(x[u].x - y.x) + ex2(x[u].y - y.y)) + (ex2(x[u].z - y.z) + ex2(x[u].w - y.w));
       }
     }
-    float* dst = p.a.weights + static_cast<long long>(bh) * p.a.weights_stride + j;
-    *dst = p.a.accumulate ? *dst + w : w;
+#pragma unroll
+    for (int u = 0; u < kKeys; ++u) {
+      if (j0 + 256 * u >= len) break;
+      float* dst = p.a.weights + static_cast<long long>(bh) * p.a.weights_stride + j0 + 256 * u;
+      *dst = p.a.accumulate ? *dst + w[u] : w[u];
+    }
   }
 }
 
@@ -919,7 +935,7 @@ int attn_run(AttnP& p, DeviceInfo* di) {
   const dim3 grid(p.grid, 8 * NT);
   if (launch_early(combine_kernel<D, NT>, grid, 128, 0, st, 1, p)) return TM_ERR_CUDA;
   if (!p.scores) return counted(2);
-  const long long want = (p.cap + 1023) / 1024;
+  const long long want = (p.cap + kKeyRun - 1) / kKeyRun;
   const dim3 wgrid(static_cast<unsigned>(want < 256 ? want : 256), a.B * a.c.Hkv);
   if (launch_early(weight_kernel<NT>, wgrid, 256, 0, st, 1, p)) return TM_ERR_CUDA;
   return counted(3);
