@@ -833,7 +833,10 @@ __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
 }
 
 // The weight of each key: sum over the kv head's rows of 2^(s - lse). A CTA takes runs
-// of 1024 keys, four a thread with their loads together.
+// of 1024 keys, four a thread with their loads together. The scores are an eighth of the
+// codes' bytes and would leave L2 for memory later; they are read here for the last time,
+// so their lines are discarded: 24 sequences of up to 32768 tokens, 4 kv heads of 7 rows,
+// take 50.6 us with it and 55.5 without.
 constexpr int kKeys = 4, kKeyRun = 256 * kKeys;
 template <int NT>
 __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
@@ -841,8 +844,10 @@ __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
   pdl_wait();
   const int bh = blockIdx.y, b = bh / p.a.c.Hkv, h = bh - b * p.a.c.Hkv;
   const long long len = min(static_cast<long long>(clamp_len(p, b)), p.a.weights_stride);
-  for (long long j0 = static_cast<long long>(blockIdx.x) * kKeyRun + threadIdx.x; j0 < len;
-       j0 += static_cast<long long>(gridDim.x) * kKeyRun) {
+  const int lane = threadIdx.x & 31;
+  for (long long jw = static_cast<long long>(blockIdx.x) * kKeyRun + threadIdx.x - lane; jw < len;
+       jw += static_cast<long long>(gridDim.x) * kKeyRun) {
+    const long long j0 = jw + lane;
     float w[kKeys] = {};
     for (int rt = 0; rt < p.RT; ++rt) {
       const long long item = static_cast<long long>(b) * p.items_per_b + h * p.RT + rt;
@@ -861,6 +866,17 @@ __global__ void __launch_bounds__(256) weight_kernel(AttnP p) {
 #pragma unroll
         for (int u = 0; u < kKeys; ++u)
           w[u] += (ex2(x[u].x - y.x) + ex2(x[u].y - y.y)) + (ex2(x[u].z - y.z) + ex2(x[u].w - y.w));
+      }
+    }
+    // 32 keys of a row tile are rs lines of 128 bytes, aligned (a page is 16 keys or more)
+    __syncwarp();
+    for (int rt = 0; rt < p.RT; ++rt) {
+      const long long item = static_cast<long long>(b) * p.items_per_b + h * p.RT + rt;
+#pragma unroll
+      for (int u = 0; u < kKeys; ++u) {
+        const long long at = (jw + 256 * u) * p.rs + 32 * lane;
+        if (lane < p.rs && at < p.cap * p.rs)
+          asm volatile("discard.global.L2 [%0], 128;" ::"l"(p.scores + item * p.cap * p.rs + at) : "memory");
       }
     }
 #pragma unroll
