@@ -574,3 +574,20 @@ def test_many_rows_take_several_tiles():
     cache = Cache(89, 2, 1, 64, 32, ref.INT8, 3)
     check_attention(cache, rand((2, 11, 3, 64), 90), [96, 7], True)
     check_attention(cache, rand((2, 1, 40, 64), 91), [96, 33], True)
+
+
+@pytest.mark.parametrize("fmt", [ref.INT8, ref.E4M3])
+@pytest.mark.parametrize("page,D", [(16, 64), (16, 128), (64, 64), (128, 128)])
+@pytest.mark.parametrize("Hq,H,nq", [(17, 1, 1), (8, 2, 8), (14, 2, 4), (3, 1, 11), (64, 2, 2)])
+def test_attention_of_many_rows(fmt, page, D, Hq, H, nq):
+    """17 to 64 rows a kv head: row tiles of 32, full and not, with queries that see nothing."""
+    mp = max(2, 320 // page)
+    cache = Cache(92 + page + D, 5, H, D, page, fmt, mp)
+    check_attention(cache, rand((5, nq, Hq, D), 93, 1.5), [mp * page, 0, 1, 5, mp * page - 7], weights=True)
+
+
+def test_attention_of_many_rows_long_and_split():
+    """32 rows: items cut between CTAs, several in one, and a page that is not there."""
+    cache = Cache(94, 4, 2, 128, 64, ref.INT8, 70)
+    cache.table[0, 3] = -1
+    check_attention(cache, rand((4, 8, 8, 128), 95, 1.5), [4480, 1, 64, 1999], weights=True)
