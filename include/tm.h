@@ -415,7 +415,7 @@ TM_API int tm_kv8_append(const void* k, const void* v, long long k_stride, long 
  *   workspace: 256-byte aligned, tm_kv8_attn_workspace_size bytes (host only);
  *     calls that share one must be ordered.
  * Results are the same from run to run. B <= 4096, B * Hkv <= 65535. The codes are
- * read once for every 16 of the nq * Hq / Hkv rows of a kv head.
+ * gone through once for every 16 of the nq * Hq / Hkv rows of a kv head.
  */
 TM_API int tm_kv8_attn_workspace_size(int B, int nq, int Hq, int Hkv, int D, int max_pages,
                                       int page, int with_weights, long long* bytes);

@@ -26,8 +26,8 @@
 // 128 x 128 tile takes 1024 clocks, twice its MMA time, so 2 of 8 exponentials
 // run on the FMA pipe (ex2x2_quintic). Four warpgroups rather than two hide the
 // dependent-issue latency of the reductions. Measured: 131072 keys, the last 256
-// queries, 32 q and 8 kv heads, D = 128: 545 us (2 x 275 GFLOP, 1.0 PFLOP/s; 1.07 G
-// exponentials a pass, 231 us of MUFU alone at 1965 MHz), 650 us under the power
+// queries, 32 q and 8 kv heads, D = 128: 560 us (2 x 275 GFLOP, 0.98 PFLOP/s; 1.07 G
+// exponentials a pass, 231 us of MUFU alone at 1965 MHz), 665 us under the power
 // cap of a long run.
 
 constexpr int kWtTiles = 4;  // A tiles, reduction warpgroups
