@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectAr
     eq_before += c[1];
   }
   for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) {  // this round's counts of each warp
+    if (rounds > 1) {  // the counts of each warp for these weights
       load(r);
       int g, e;
       count(g, e);
