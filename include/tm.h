@@ -333,7 +333,10 @@ enum { TM_ROPE_HALF = 0, TM_ROPE_INTERLEAVED = 1 };
  *   rot: even, 2 .. D. Any D that is a multiple of 16, up to 512.
  *   strides: elements between consecutive tokens, multiples of 8 and at least
  *     heads * D, so that q and k may be read out of (or turned inside) a packed
- *     q/k/v buffer; batches follow each other, N rows each.
+ *     q/k/v buffer; batches follow each other, N rows each. With N = 1 the
+ *     stride is therefore the one between the sequences' rows (a tensor's own
+ *     stride between tokens means nothing there; the Python binding does not
+ *     take it for one).
  *   q_out may be q itself and k_out k itself (same stride: in place), but no
  *     output may otherwise overlap an input or the other output. k and k_out may
  *     be NULL with Hkv = 0, q and q_out NULL with Hq = 0.

@@ -394,9 +394,33 @@ def _device_ptrs(*xs):
     return out
 
 
+def _rows_apart(x, name, B, N, stride):
+    """Elements between consecutive rows of x, whose B sequences of N rows follow each other:
+    ``stride``. Where a tensor [B, N, ...] has its rows elsewhere the call is refused, except
+    that one row a sequence has no stride of its own (torch may report any): there the stride
+    between sequences counts."""
+    try:
+        own = x.stride()
+    except AttributeError:
+        return stride  # an address, or nothing
+    if len(own) < 3 or x.shape[0] != B or x.shape[1] != N:
+        return stride  # a buffer of another shape that the number says how to read
+    if N == 1:
+        if B == 1 or stride in own[:2]:
+            return stride if B == 1 else own[0]
+    elif stride == own[1] and (B == 1 or own[0] == N * stride):
+        return stride
+    raise ValueError(f"{name}: rows {stride} elements apart do not lie where the strides {own} of "
+                     f"its {tuple(x.shape)} put them")
+
+
 def tm_rope_fwd(q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_stride,
                 k_out_stride, rot, layout, inverse, inv_freq, mscale, positions, first,
                 stream=None):
+    q_stride = _rows_apart(q, "q", B, N, q_stride)
+    q_out_stride = _rows_apart(q_out, "q_out", B, N, q_out_stride)
+    k_stride = _rows_apart(k, "k", B, N, k_stride)
+    k_out_stride = _rows_apart(k_out, "k_out", B, N, k_out_stride)
     q, q_out, k, k_out, f, pos = _device_ptrs(q, q_out, k, k_out, inv_freq, positions)
     return _check("tm_rope_fwd", lib().tm_rope_fwd(
         q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_stride, k_out_stride, rot,

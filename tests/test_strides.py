@@ -1,0 +1,68 @@
+"""The strides that the raw calls pass on, without a GPU: a tensor [B, N, ...] whose
+rows lie elsewhere than the number says is read where its rows are, or refused."""
+import pytest
+
+import long_context_prefill_trianglemix_b200 as tm
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Every call of the library as (name, arguments); tensors pass for addresses."""
+    made = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: made.append((name, args)) or tm.TM_OK
+
+    monkeypatch.setattr(tm, "lib", lambda: Library())
+    monkeypatch.setattr(tm, "_device_ptrs", lambda *xs: [x if x is None else x.data_ptr() for x in xs])
+    monkeypatch.setattr(tm, "_stream", lambda s: 0)
+    return made
+
+
+def packed(B, N, Hq, Hkv, D):
+    import torch
+    x = torch.zeros((B, N, (Hq + 2 * Hkv) * D), dtype=torch.bfloat16)
+    return [t.view(B, N, -1, D) for t in x.split([Hq * D, Hkv * D, Hkv * D], -1)]
+
+
+def rope(q, k, q_stride, k_stride, qo=None, ko=None, strides=None):
+    import torch
+    B, N, Hq, D = q.shape
+    Hkv = k.shape[2]
+    qo = torch.zeros((B, N, Hq, D), dtype=torch.bfloat16) if qo is None else qo
+    ko = torch.zeros((B, N, Hkv, D), dtype=torch.bfloat16) if ko is None else ko
+    f = torch.zeros(D // 2, dtype=torch.float64)
+    tm.tm_rope_fwd(q, qo, k, ko, B, N, Hq, Hkv, D, q_stride, *(strides or (Hq * D,)), k_stride,
+                   *(strides or (Hkv * D,)), D, 0, 0, f, 1.0, None, 0)
+
+
+def test_rope_of_one_token_passes_the_stride_between_sequences(calls):
+    q, k, _ = packed(3, 1, 4, 2, 64)
+    assert q.stride(1) != q.stride(0) == 512
+    rope(q, k, q.stride(1), k.stride(1))
+    rope(q, k, q.stride(0), 512)
+    rope(q, k, q.stride(1), k.stride(1), q, k, (512,))
+    for name, args in calls:
+        assert name == "tm_rope_fwd" and args[9] == 512 and args[11] == 512
+    assert [args[10] for _, args in calls] == [256, 256, 512]
+    assert [args[12] for _, args in calls] == [128, 128, 512]
+
+
+def test_rope_of_several_tokens_passes_its_numbers_on(calls):
+    q, k, _ = packed(3, 5, 4, 2, 64)
+    rope(q, k, 512, 512)
+    flat = q[:1]
+    rope(flat, k[:1], 512, 512)
+    assert [(args[9], args[11]) for _, args in calls] == [(512, 512)] * 2
+
+
+def test_rope_refuses_rows_that_are_elsewhere(calls):
+    q, k, _ = packed(3, 5, 4, 2, 64)
+    for bad in [lambda: rope(q, k, 256, 512), lambda: rope(q, k, 512, 1024),
+                lambda: rope(q[:, :4], k[:, :4], 512, 512),          # batches do not follow each other
+                lambda: rope(q[:, :1], k[:, :1], 256, 512)]:
+        with pytest.raises(ValueError, match="apart"):
+            bad()
+    rope(q[:, :1], k[:, :1], 512, 512)      # one row each: five packed rows apart
+    assert [(args[9], args[11]) for _, args in calls] == [(2560, 2560)]
