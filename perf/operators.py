@@ -216,8 +216,6 @@ def prepare(case, seed):
         else:
             s["q"] = _random(g, (B, N, Hq, D), 2.0).to(torch.bfloat16)
             s["k"] = _random(g, (B, N, Hkv, D), 2.0).to(torch.bfloat16)
-        s["q_stride"] = width or Hq * D     # elements between tokens (a one-token tensor's own
-        s["k_stride"] = width or Hkv * D    # stride need not say it)
         s["q_out"] = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device="cuda")
         s["k_out"] = torch.empty((B, N, Hkv, D), dtype=torch.bfloat16, device="cuda")
         s["inv_freq"] = _inv_freq(c)
@@ -303,8 +301,8 @@ def _rope(s):
     if own:
         import long_context_prefill_trianglemix_b200 as tm
         tm.tm_rope_fwd(q, s["q_out"], k, s["k_out"], c["B"], c["N"], c["Hq"], c["Hkv"], D,
-                       s["q_stride"], c["Hq"] * D, s["k_stride"], c["Hkv"] * D, rot, c["layout"],
-                       0, s["inv_freq"], s["mscale"], s["positions"], s["first"])
+                       q.stride(1), c["Hq"] * D, k.stride(1), c["Hkv"] * D, rot, c["layout"], 0,
+                       s["inv_freq"], s["mscale"], s["positions"], s["first"])
         return s["q_out"], s["k_out"]
     pos = s["positions"]
     if pos is None:
