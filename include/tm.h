@@ -386,7 +386,8 @@ enum { TM_KV_INT8 = 0, TM_KV_E4M3 = 1 };
  * nearest, ties to even. The call neither changes lens nor reads ranges of
  * blocks that held no token, and rows behind the last token keep their bytes.
  *   k, v: bf16 [B, n_src, Hkv, D], k_stride / v_stride elements between tokens
- *     (multiples of 8, at least Hkv * D), n_src tokens per sequence.
+ *     (multiples of 8, at least Hkv * D), n_src tokens per sequence; with
+ *     n_src = 1 between the sequences' rows, as for tm_rope_fwd.
  *   counts: int32 [B] or NULL: only the first counts[b] (clamped to [0, n]) of
  *     the n tokens are stored. NULL: n.
  *   index: int32 [B, Hkv, n] or NULL: token i of head h is row index[b, h, i]

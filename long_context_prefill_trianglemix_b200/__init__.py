@@ -438,6 +438,8 @@ def tm_rope_inv_freq(rot, base, factor=1.0, trained_len=1.0, low_turns=0.0,
 
 def tm_kv8_append(k, v, k_stride, v_stride, B, n_src, n, Hkv, D, counts, index, lens, table,
                   max_pages, k8, v8, k_range, v_range, num_pages, page, format, stream=None):
+    k_stride = _rows_apart(k, "k", B, n_src, k_stride)
+    v_stride = _rows_apart(v, "v", B, n_src, v_stride)
     k, v, counts, index, lens, table, k8, v8, k_range, v_range = _device_ptrs(
         k, v, counts, index, lens, table, k8, v8, k_range, v_range)
     return _check("tm_kv8_append", lib().tm_kv8_append(

@@ -72,3 +72,35 @@ def test_rope_of_one_token_a_sequence(B, Hq, Hkv, D, rot, layout):
                    yk.stride(1), rot, layout, 0, df, 1.0, dp, 0)
     assert torch.equal(yq, first[0]) and torch.equal(yk, first[1])
     assert torch.equal(y[..., (Hq + Hkv) * D:], x[..., (Hq + Hkv) * D:])
+
+
+@pytest.mark.parametrize("fmt", [ref.INT8, ref.E4M3])
+@pytest.mark.parametrize("B,Hq,Hkv,D,page", [(2, 4, 2, 64, 16), (33, 32, 8, 128, 64), (5, 7, 1, 128, 32),
+                                             (1, 8, 2, 64, 128)])
+def test_append_of_one_token_a_sequence(B, Hq, Hkv, D, page, fmt):
+    """k and v stay in the packed projection; codes and ranges bit for bit, twice in a row (the
+    second token meets a block that holds the first)."""
+    import torch
+    shape, codes = (2 * B, Hkv, page, D), torch.int8 if fmt == ref.INT8 else torch.float8_e4m3fn
+    table = torch.randperm(2 * B, generator=torch.Generator().manual_seed(B)).to(torch.int32)
+    table = table.view(B, 2).cuda()
+    start = np.random.default_rng(B).integers(0, 2 * page - 2, B)
+    wk = wv = (np.zeros(shape), np.zeros(shape[:2]))
+    caches = [tm.Kv8Cache.empty(2 * B, Hkv, page, D, fmt) for _ in range(4)]
+    for step in range(2):
+        _, _, k, v = packed(B, Hq, Hkv, D, 100 * B + step)
+        lens, W = start + step, (Hq + 2 * Hkv) * D
+        dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        args = [(k.double().cpu().numpy(), *wk), (v.double().cpu().numpy(), *wv)]
+        wk, wv = (ref.append(x, lens, [1] * B, table.cpu().numpy(), c, r, fmt) for x, c, r in args)
+        for c, strides in zip(caches, ((k.stride(1), v.stride(1)), (k.stride(0), v.stride(0)), (W, W), None)):
+            if strides is None:
+                tm.kv8_append(c, k, v, dl, table)
+            else:
+                if B == 1 and strides[0] < Hkv * D:
+                    strides = W, W
+                tm.tm_kv8_append(k, v, *strides, B, 1, 1, Hkv, D, None, None, dl, table, 2, *c, 2 * B,
+                                 page, fmt)
+            for got, want in ((c.k8, wk[0]), (c.v8, wv[0]), (c.k_range, wk[1]), (c.v_range, wv[1])):
+                np.testing.assert_array_equal(got.float().cpu().numpy(), want)
+            assert c.k8.dtype == codes

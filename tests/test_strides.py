@@ -66,3 +66,31 @@ def test_rope_refuses_rows_that_are_elsewhere(calls):
             bad()
     rope(q[:, :1], k[:, :1], 512, 512)      # one row each: five packed rows apart
     assert [(args[9], args[11]) for _, args in calls] == [(2560, 2560)]
+
+
+def append(k, v, k_stride, v_stride, n=None):
+    import torch
+    B, n_src, H, D = k.shape
+    i32, page = torch.zeros(B, dtype=torch.int32), torch.zeros((4, H, 16, D), dtype=torch.int8)
+    r = torch.zeros((4, H))
+    tm.tm_kv8_append(k, v, k_stride, v_stride, B, n_src, n or n_src, H, D, None, None, i32,
+                     i32.view(B, 1), 1, page, page, r, r, 4, 16, 0)
+
+
+def test_append_of_one_token_passes_the_stride_between_sequences(calls):
+    _, k, v = packed(3, 1, 4, 2, 64)
+    append(k, v, k.stride(1), v.stride(1))
+    append(k, v, 512, v.stride(0))
+    _, k, v = packed(3, 5, 4, 2, 64)
+    append(k, v, 512, 512, 4)
+    append(k[:, 2:3], v[:, :1], 512, 2560)
+    assert [args[2:4] for _, args in calls] == [(512, 512)] * 3 + [(2560, 2560)]
+
+
+def test_append_refuses_rows_that_are_elsewhere(calls):
+    _, k, v = packed(3, 5, 4, 2, 64)
+    for bad in [lambda: append(k, v, 128, 512), lambda: append(k, v, 512, 128),
+                lambda: append(k[:, :4], v[:, :4], 512, 512), lambda: append(k[:, :1], v[:, :1], 2560, 128)]:
+        with pytest.raises(ValueError, match="apart"):
+            bad()
+    assert not calls
