@@ -456,7 +456,8 @@ TM_API int tm_key_weights_fwd(const void* q, const void* k, int B, int Hq, int H
  *   weights: fp32 [B, H, weights_stride >= n].
  *   index: int32 [B, H, keep], ascending, -1 behind the kept ones.
  *   kept: int32 [B] (may be NULL): min(lens[b], keep).
- * sinks >= 0, recent >= 0, sinks + recent <= keep, keep >= 1, n >= 1.
+ * sinks >= 0, recent >= 0, sinks + recent <= keep, keep >= 1, n >= 1; n and keep
+ * at most 2^31 - 1 - 65536.
  */
 TM_API int tm_kv_select(const float* weights, long long weights_stride, const int* lens, int B,
                         int H, int n, int keep, int sinks, int recent, int* index, int* kept,

@@ -349,8 +349,10 @@ TM_API int tm_kv_select(const float* weights, long long weights_stride, const in
   if (!weights || !index || B < 1 || H < 1 || n < 1 || keep < 1 || sinks < 0 || recent < 0)
     return TM_ERR_INVALID_ARG;
   if (static_cast<long long>(sinks) + recent > keep || weights_stride < n ||
-      weights_stride > kIntMax || n > kIntMax - 65536)
+      weights_stride > kIntMax)
     return TM_ERR_INVALID_ARG;
+  // the kernel's loops over n and keep step by a cluster's threads or keys, in 32 bits
+  if (n > kIntMax - 65536 || keep > kIntMax - 65536) return TM_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(B) * H;
   if (rows > kIntMax / 8 || B > 65535 || 2LL * H > 65535) return TM_ERR_INVALID_ARG;
   if (!aligned(weights, 4) || !aligned(lens, 4) || !aligned(index, 4) || !aligned(kept, 4))
