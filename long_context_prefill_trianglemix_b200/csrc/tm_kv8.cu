@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(BW > 4 ? BW * 32 : 128) append_kernel(const Ap
       const uint16_t* at = src + (tok0 + t / RC) * stride;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        x[i] = __ldg(reinterpret_cast<const uint4*>(at));
+        x[i] = *reinterpret_cast<const uint4*>(at);
         at += STEP * stride;
       }
     } else {
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(BW > 4 ? BW * 32 : 128) append_kernel(const Ap
           long long tok = tok0 + row;
           if (index) tok = index[tok];
           if (tok >= 0 && tok < a.n_src)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(src + tok * stride));
+            x[i] = *reinterpret_cast<const uint4*>(src + tok * stride);
         }
       }
     }

@@ -183,7 +183,7 @@ __device__ __forceinline__ UnitAt locate(const AttnP& p, const int* pre, int x, 
   at.u = x - pre[lo] - it * U;
   at.item = lo * p.items_per_b + it;
   const int tok0 = at.u * 16 * UT;
-  const int page = __ldg(p.a.table + static_cast<long long>(lo) * p.a.max_pages + (tok0 >> p.page_log));
+  const int page = p.a.table[static_cast<long long>(lo) * p.a.max_pages + (tok0 >> p.page_log)];
   if (static_cast<unsigned>(page) < static_cast<unsigned>(p.a.c.num_pages)) {
     const long long block = static_cast<long long>(page) * p.a.c.Hkv + it / p.RT;
     at.row = static_cast<int>(((block << p.page_log) + (tok0 & (p.a.c.page - 1))) / (128 / D));
@@ -195,8 +195,8 @@ template <int D>
 __device__ __forceinline__ void load_ranges(const AttnP& p, UnitAt& at) {
   if (at.row < 0) return;
   const long long block = (static_cast<long long>(at.row) * (128 / D)) >> p.page_log;
-  at.kr = __ldg(p.a.c.k_range + block);
-  at.vr = __ldg(p.a.c.v_range + block);
+  at.kr = p.a.c.k_range[block];
+  at.vr = p.a.c.v_range[block];
 }
 
 // Prefix sums of the sequences' units (times items per sequence) in shared memory;
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
         }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          w[j] = q ? __ldg(reinterpret_cast<const uint4*>(q + 8 * j)) : make_uint4(0, 0, 0, 0);
+          w[j] = q ? *reinterpret_cast<const uint4*>(q + 8 * j) : make_uint4(0, 0, 0, 0);
           mx = __vmaxu2(mx, __vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu));
           mx = __vmaxu2(mx, __vmaxu2(w[j].z & 0x7FFF7FFFu, w[j].w & 0x7FFF7FFFu));
         }

@@ -6,6 +6,9 @@
 // memory and before it returns: the wait ends when the kernel ahead has completed
 // and its writes are visible, and so, because that kernel waited too, everything
 // before it. pdl_launch() lets the kernel behind take its place early.
+// Such a kernel reads with plain loads (or TMA) only: the read-only path (__ldg) is
+// for memory that does not change from a kernel's start on, and its start comes
+// before the writes of the kernel ahead.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -97,13 +97,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const KvSelectAr
     if (base + kRun <= hi) {
       float x[KPL];
 #pragma unroll
-      for (int k = 0; k < KPL; ++k) x[k] = __ldg(at + 32 * k);
+      for (int k = 0; k < KPL; ++k) x[k] = at[32 * k];
 #pragma unroll
       for (int k = 0; k < KPL; ++k) key[k] = sort_key(x[k]);
     } else {
 #pragma unroll
       for (int k = 0; k < KPL; ++k)
-        key[k] = base + 32 * k + lane < hi ? sort_key(__ldg(at + 32 * k)) : 0u;
+        key[k] = base + 32 * k + lane < hi ? sort_key(at[32 * k]) : 0u;
     }
     if (base < a.sinks || base + kRun > n - a.recent) {
 #pragma unroll
