@@ -403,12 +403,16 @@ def _rows_apart(x, name, B, N, stride):
         own = x.stride()
     except AttributeError:
         return stride  # an address, or nothing
-    if len(own) < 3 or x.shape[0] != B or x.shape[1] != N:
-        return stride  # a buffer of another shape that the number says how to read
     if N == 1:
-        if B == 1 or stride in own[:2]:
-            return stride if B == 1 else own[0]
-    elif stride == own[1] and (B == 1 or own[0] == N * stride):
+        if stride == own[0] or B == 1:
+            return stride
+        shape = x.shape
+        if len(own) < 3 or shape[0] != B or shape[1] != 1:
+            return stride  # a buffer of another shape that the number says how to read
+        if stride == own[1]:
+            return own[0]
+    elif len(own) < 3 or x.size(0) != B or x.size(1) != N or (
+            stride == own[1] and (B == 1 or own[0] == N * stride)):
         return stride
     raise ValueError(f"{name}: rows {stride} elements apart do not lie where the strides {own} of "
                      f"its {tuple(x.shape)} put them")
