@@ -409,8 +409,10 @@ TM_API int tm_kv8_append(const void* k, const void* v, long long k_stride, long 
  * first). q, o: bf16 [B, nq, Hq, D]; Hq % Hkv == 0; nq >= 1. lens is clamped to
  * [0, max_pages * page]; a row that sees no key is written as zeros. Scores,
  * softmax and sums are fp32, the weights fp16 at a scale that keeps 11 bits of
- * every weight above 2^-22 of the row's largest, K, V and q enter the products
- * exactly.
+ * every weight above 2^-22 of the row's largest (less ones are off by 2^-33 of
+ * it). K, V and q enter the products exactly, but for elements of q below 2^-31
+ * of their row's largest, which are rounded by at most 2^-39 of it. A block whose
+ * V range is less than 2^-70 of another of the sequence's may add nothing.
  *   weights: fp32 [B, Hkv, weights_stride] or NULL. The attention weight of key
  *     j < lens[b], summed over the nq rows and the q heads of the group, is
  *     stored at [b, h, j], or added to what is there if accumulate != 0.

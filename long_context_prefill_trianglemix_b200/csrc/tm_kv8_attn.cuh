@@ -22,14 +22,15 @@
 // - Codes become fp16 exactly (int8 by 1024 + u in the low mantissa bits, e4m3 by
 //   the conversion instruction). q becomes fp16 after an exact scaling of the
 //   row by a power of two that brings its largest element to [2^14, 2^15):
-//   fp16's 11 bits hold bf16's 8, and elements 2^-29 of the largest or less are
-//   rounded by at most 2^-40 of it. Products and sums are fp32.
-// - P is fp16, scaled by 2^8 against the running reference and allowed to grow
-//   to 2^15, and carries V's range, kept within 2^-10 of a reference of its own:
-//   weights down to 2^-22 of the largest keep fp16's 11 bits (rounding 2^-11 of each
-//   weight, below the bf16 output's 2^-8), less ones are off by 2^-33 of the largest.
-//   The reference moves only when a score exceeds it by more than 7 (log2), so the
-//   usual unit needs one vote and no rescale; m, l and O are fp32.
+//   fp16's 11 bits hold bf16's 8, and elements below 2^-31 of the largest are
+//   rounded by at most 2^-39 of it. Products and sums are fp32.
+// - P is fp16, scaled by 2^11 against the running reference and allowed to grow
+//   to 2^14.5, and carries V's range over a power of two, a factor of 2^-3 to 2:
+//   weights down to 2^-22 of the largest keep fp16's 11 bits (2^-22 2^11 2^-3 is its
+//   least normal number; rounding 2^-11 of each weight, below the bf16 output's 2^-8),
+//   less ones are off by 2^-33 of the largest. The reference moves only when a score
+//   exceeds it by more than 3.5 (log2), the power of two when a range leaves its
+//   window, so the usual unit needs one vote and no rescale; m, l and O are fp32.
 //
 // Parts of an item (sequence, kv head, row tile) that end in one CTA are merged
 // there; an item cut between CTAs leaves unnormalised partials (O, m, l) in the
@@ -44,10 +45,11 @@ using namespace kv8;
 constexpr int kWarps = 8;       // of a CTA
 constexpr int kMaxAttnBatch = 4096;
 constexpr int kMaxSms = 192;    // workspaces are sized for this many
-constexpr float kLift = 8.f;    // log2 of the scale of P against the reference
-constexpr float kSlack = 7.f;   // scores may exceed the reference by this
-constexpr float kFar = 0x1p-10f;  // P takes a V range in while it is this much of the reference
-constexpr float kFarthest = 0x1p-70f;  // (further below the largest it adds nothing fp32 would hold)
+constexpr float kLift = 11.f;   // log2 of the scale of P against the reference
+constexpr float kSlack = 3.5f;  // scores may exceed the reference by this
+constexpr float kFar = 0x1p-3f;   // P takes a V range in while it is this much of V's reference
+constexpr float kFarthest = 0x1p-70f;  // a range this far below the part's largest is taken as 0: O, at
+                                       // most 2^55 for 2^31 keys, must not overflow as it is rescaled
 constexpr float kLowest = -1.7e38f;
 
 struct AttnP {
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
   uint32_t qf[NT][D / 16][2];
   // shift = kLift - reference; O = acc * vref / F
   float sc[NT][2], acc[NT][D / 16][4], ref[NT][2], shift[NT][2], l[NT][2];
-  float vref = 0.f, iref = 0.f, vtop = 0.f;  // V's reference range, 1 / it, the largest so far
+  float vref = 0.f, iref = 0.f, vtop = 0.f;  // V's reference (a power of two), 1 / it, its largest so far
   int lim[NT][2];
   float* scores = nullptr;
   bool ok = true;
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       U = (len + C::kUnit - 1) / C::kUnit;
       left = min(U - u, n_units - i);
       scores = p.scores ? p.scores + static_cast<long long>(item) * p.cap * p.rs : nullptr;
-      vref = vtop = 0.f;
+      vref = iref = vtop = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = row0 + 8 * n + g;
@@ -491,14 +493,16 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
         for (int e = 0; e < 4; ++e) x[0][n][e] += x2[n][e];
     // keys up to len - nq are seen by every row
     const bool edge = tok0 + C::kUnit - 1 > len - a.nq || !there;
-    // V's ranges: P carries vr / vref (at most 1 and at least 2^-10, so that fp16 holds it as
+    // V's ranges: P carries vr / vref (less than 2 and at least 2^-3, so that fp16 holds it much as
     // it would hold P) and O accumulates in the products; vref moves when a range leaves that
-    // window. Infinite and NaN ranges stay out of vref: they are for their rows alone.
-    if ((vr > vref || (vr < vref * kFar && vr > vtop * kFarthest)) && vr <= 3.4028234e38f) {
-      const float f = vref / vr;
-      vref = vr;
-      vtop = fmaxf(vtop, vr);
-      iref = 1.f / vr;
+    // window, by powers of two, so that O is rescaled exactly however often ranges alternate.
+    // Infinite and NaN ranges stay out of vref: they are for their rows alone.
+    if ((vr >= 2.f * vref || (vr < vref * kFar && vr > vtop * kFarthest)) && vr <= 3.4028234e38f) {
+      const float to = __uint_as_float(max(__float_as_uint(vr) & 0x7F800000u, 0x00800000u));
+      const float f = vref / to;
+      vref = to;
+      vtop = fmaxf(vtop, to);
+      iref = 1.f / to;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[n][m][e] *= f;
     }
-    const float rho = vr == vref ? 1.f : vref > 1e-30f ? vr * iref : vref > 0.f ? vr / vref : vr;
+    const float rho = vr * iref;  // (NaN where no range was finite yet)
     bool over = !here;
     float f[NT][2], pv[NT][2];
 #pragma unroll
