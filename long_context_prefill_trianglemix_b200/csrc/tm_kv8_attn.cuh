@@ -34,7 +34,9 @@
 //
 // Parts of an item (sequence, kv head, row tile) that end in one CTA are merged
 // there; an item cut between CTAs leaves unnormalised partials (O, m, l) in the
-// workspace and combine_kernel joins them in order, so results are reproducible.
+// workspace and combine_kernel joins them in order, so results are reproducible. O is
+// a sum of up to 2^14.5 times the item's keys of V's values: a partial takes 2^-s of
+// it with 2^s above that, so that V near its type's largest value does not overflow.
 // Included by tm_attn.cu inside namespace trimix (status word, bounded waits, TMA
 // helpers, tensor-map encoding).
 
@@ -60,7 +62,7 @@ struct AttnP {
   float2* part_ml;    // [2 grid][8 NT]
   float* warp_o;      // [grid][warps][8 NT][D]: a warp's first partial
   int4* close;        // [grid]: the item from an earlier CTA that ends in this one (item, first CTA,
-                      // its slot, last CTA), or -1
+                      // its slot and, above 16 bits, the item's s, last CTA), or -1
   float* lse;         // [items][8 NT] (log2), +inf where a row keeps nothing
   float* scores;      // [items][cap][rs] (log2), or null
   int rs;             // rows kept of a token's scores: those of an item, to a multiple of 4
@@ -239,6 +241,14 @@ __device__ __forceinline__ int unit_prefix(const AttnP& p, int* pre) {
   return most;
 }
 
+// The exponent s above for an item of U units of `unit` tokens (20 to 47), and 2^s.
+__device__ __forceinline__ int sum_bits(int U, int unit) {
+  return 47 - __clz(static_cast<unsigned>(U) * static_cast<unsigned>(unit));
+}
+__device__ __forceinline__ float power_of_two(int s) {
+  return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
+}
+
 __device__ __forceinline__ void store_bf16(uint16_t* dst, float a, float b) {
   *reinterpret_cast<uint32_t*>(dst) = sm100::pack_bf16x2(a, b);
 }
@@ -336,8 +346,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       if (U0 + U <= ce) {
         // the part that holds unit U0: the last c with floor(c T / parts) <= U0
         const int c0 = static_cast<int>(((U0 + 1LL) * parts - 1) / T);
-        rec = make_int4(sb * p.items_per_b + (U0 - pre[sb]) / U, c0, 2 * c0 + (T * c0 / parts < U0),
-                        cta);
+        rec = make_int4(sb * p.items_per_b + (U0 - pre[sb]) / U, c0,
+                        (2 * c0 + (T * c0 / parts < U0)) | sum_bits(U, C::kUnit) << 16, cta);
       }
     }
     p.close[cta] = rec;
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
           uint16_t* dst = out_row<D>(p, b, h, rr) + g * (D / 8);
 #pragma unroll
           for (int m = 0; m < D / 16; ++m)
-            store_bf16(dst + 2 * m, acc[n][m][e] * vs * inv, acc[n][m][e + 2] * vs * inv);
+            store_bf16(dst + 2 * m, acc[n][m][e] * inv * vs, acc[n][m][e + 2] * inv * vs);
         }
     } else {
       // slot 0 (more items follow, the ring is in use): global scratch; slot 1 (the
@@ -660,6 +670,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
       float* o = last ? reinterpret_cast<float*>(ring)
                       : p.warp_o + (static_cast<long long>(cta) * W + warp) * 8 * NT * D;
       if (lane == 0) s_item[slot] = item;
+      const float down = power_of_two(-sum_bits(U, C::kUnit));
       __syncwarp();  // every lane has read the last unit
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -670,7 +681,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
           float2* dst = reinterpret_cast<float2*>(o + c * D + g * (D / 8));
 #pragma unroll
           for (int m = 0; m < D / 16; ++m)
-            dst[m] = make_float2(acc[n][m][e] * vs, acc[n][m][e + 2] * vs);
+            dst[m] = make_float2(acc[n][m][e] * down * vs, acc[n][m][e + 2] * down * vs);
         }
     }
   }
@@ -753,7 +764,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, UT>::kThreads, AttnCfg<D, NT, U
         p.lse[static_cast<long long>(it_id) * (8 * NT) + c] =
             some && rr < p.rows ? m - kLift + log2f(ls) : INFINITY;
       if (rr < p.rows) {
-        const float inv = some ? 1.f / ls : 0.f;
+        const float inv = some ? power_of_two(sum_bits(U, C::kUnit)) / ls : 0.f;
         *reinterpret_cast<uint2*>(out_row<D>(p, ib, hh, rr) + 4 * d4) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
       }
@@ -775,7 +786,7 @@ __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
   pdl_wait();
   const int4 rec = p.close[blockIdx.x];
   if (rec.x < 0) return;
-  const int item = rec.x, c0 = rec.y, first = rec.z, c1 = rec.w;
+  const int item = rec.x, c0 = rec.y, first = rec.z & 0xFFFF, c1 = rec.w;
   const int ib = item / p.items_per_b, it = item - ib * p.items_per_b;
   const int h = it / p.RT, rt = it - h * p.RT, rr = rt * 8 * NT + c;
   __shared__ float4 s_o[GR][V];
@@ -831,7 +842,7 @@ __global__ void __launch_bounds__(128) combine_kernel(AttnP p) {
   if (p.lse && lane4 == 0)
     p.lse[static_cast<long long>(item) * (8 * NT) + c] = some && rr < p.rows ? m - kLift + log2f(l) : INFINITY;
   if (rr >= p.rows) return;
-  const float inv = some ? 1.f / l : 0.f;
+  const float inv = some ? power_of_two(rec.z >> 16) / l : 0.f;
   *reinterpret_cast<uint2*>(out_row<D>(p, ib, h, rr) + 4 * lane4) =
       make_uint2(sm100::pack_bf16x2(o.x * inv, o.y * inv), sm100::pack_bf16x2(o.z * inv, o.w * inv));
 }

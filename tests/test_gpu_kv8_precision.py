@@ -64,3 +64,19 @@ def test_small_weights_beside_a_larger_range(fmt, D, nq):
         bound = want * 2.0 ** -8 + mass * (2.0 ** -11 + 2 * (np.abs(s).max() * 2.0 ** -20 + 2.0 ** -21))
         err = np.abs(got[:, i] - want)
         assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("fmt", [ref.INT8, ref.E4M3])
+@pytest.mark.parametrize("nq", [1, 3])
+def test_values_near_the_largest(fmt, nq):
+    """V of 2^120 to 2^126: o is finite and as precise as for V of ordinary size (its bits are the
+    same but for the exponent), in items of one warp, of one CTA and cut between CTAs."""
+    import torch
+    cache = Cache(130, 6, 2, 128, 64, fmt, 70)
+    q, lens = rand((6, nq, 8, 128), 131, 1.5), ints([4480, 1, 63, 64, 65, 1999])
+    cache.vr.copy_(2.0 ** torch.randint(-3, 2, cache.vr.shape, device="cuda").float())
+    want = cache.attend(q, lens)
+    cache.vr.mul_(2.0 ** 125)
+    got = cache.attend(q, lens)
+    assert torch.isfinite(got).all()
+    assert torch.equal(got.double() * 2.0 ** -125, want.double())
