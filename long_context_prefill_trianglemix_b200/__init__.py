@@ -431,9 +431,12 @@ def tm_rope_fwd(q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_
         layout, int(inverse), f, mscale, pos, first, _stream(stream)))
 
 
-def tm_rope_inv_freq(rot, base, factor=1.0, trained_len=1.0, low_turns=0.0,
-                     high_turns=0.0) -> np.ndarray:
-    """The rotary frequencies (fp64, on the host), stretched by ``factor`` for long contexts."""
+def tm_rope_inv_freq(rot, base, factor=1.0, trained_len=1.0, low_turns=math.inf,
+                     high_turns=None) -> np.ndarray:
+    """The rotary frequencies (fp64, on the host), stretched by ``factor`` for long contexts: every
+    pair, or those of few turns over trained_len where a band of turns is given (high_turns:
+    low_turns unless given)."""
+    high_turns = low_turns if high_turns is None else high_turns
     out = np.zeros(max(int(rot) // 2, 1), np.float64)
     _check("tm_rope_inv_freq", lib().tm_rope_inv_freq(rot, base, factor, trained_len, low_turns,
                                                       high_turns, out.ctypes.data))
