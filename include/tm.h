@@ -324,10 +324,11 @@ enum { TM_ROPE_HALF = 0, TM_ROPE_INTERLEAVED = 1 };
  * the pair (a, b) number i < rot / 2 turns by t = pos * inv_freq[i]:
  *   y_a = mscale (x_a cos t - x_b sin t),   y_b = mscale (x_b cos t + x_a sin t)
  * and columns from rot on are copied. pos = positions[b * N + n] (int32, any
- * value), or first + n where positions is NULL. inverse != 0 turns by -t (the
- * transpose: it takes a rotation back when mscale is 1, and maps gradients).
- * The angle is formed and reduced in fp64; the rotation is fp32, rounded to
- * bf16 once.
+ * value), or first + n where positions is NULL (|first| <= 2^52). inverse != 0
+ * turns by -t (the transpose: it takes a rotation back when mscale is 1, and maps
+ * gradients). The angle is formed and reduced in fp64, far ones with the rounding
+ * errors carried, to 2^-23 of a turn at every position (for |inv_freq| <= 1); the
+ * rotation is fp32, rounded to bf16 once.
  *   inv_freq: rot / 2 doubles; tm_rope_inv_freq fills a host array with the
  *     usual ones, frequencies stretched for long contexts among them.
  *   rot: even, 2 .. D. Any D that is a multiple of 16, up to 512.

@@ -6,8 +6,13 @@
 // with the pair (a, b) = (i, i + rot/2) (half layout) or (2i, 2i + 1)
 // (interleaved) and t = pos * inv_freq[i]. Far positions make t large (10^5 to
 // 10^6 radians), where fp32 has no digits left for the fraction of a turn, so
-// pos * inv_freq / (2 pi) is formed and reduced to [-1/2, 1/2] turns in fp64
-// and only the remainder goes to fp32 (error below 2^-24 of a turn).
+// pos * inv_freq / (2 pi) is formed and reduced to [-1/2, 1/2] turns in fp64 and only
+// the remainder goes to fp32. For positions of 32 bits one double is enough (three
+// roundings of 2^-53 of 2^28.4 turns, and fp32's: an error below 2^-23 of a turn). A
+// call whose `first` lies beyond takes kernels that carry what the products' roundings
+// dropped in a second double: the same bound up to 2^52, where one double would be 1/8
+// of a turn off. Carried always, it costs 2 x 4173 rows of half-turned heads 17.0 us
+// instead of 16.05; behind a branch on the position, 17.3.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,9 +40,13 @@ struct RopeParams {
   long long first;
 };
 
+template <bool FAR>
 __device__ __forceinline__ void angle(const RopeParams& p, double pos, int i, float& c, float& s) {
-  const double turns = pos * p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-  const float half_turns = static_cast<float>(2.0 * (turns - rint(turns)));
+  constexpr double kInv = 0.15915494309189533577, kInvLow = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double f = p.inv_freq[i], t = pos * f, turns = t * kInv;
+  double rest = turns - rint(turns);
+  if (FAR) rest += fma(t, kInv, -turns) + fma(t, kInvLow, fma(pos, f, -t) * kInv);
+  const float half_turns = static_cast<float>(2.0 * rest);
   sincospif(half_turns, &s, &c);
   c *= p.mscale;
   s *= p.mscale * p.sign;
@@ -84,6 +93,7 @@ __device__ __forceinline__ void turn16(uint4& u, uint4& v, const float (&c)[8], 
 // work is shared by up to Hq + Hkv heads. D / 16 neighbouring threads cover a
 // head's row: 128-byte runs of loads and stores. rot is a multiple of 16. Memory
 // bounds it: 131072 tokens of 32 + 8 heads of 128 take 411 us (6.53 TB/s).
+template <bool FAR>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
   pdl_launch();
   pdl_wait();
@@ -118,7 +128,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
     if (hb == h0 && turns) {
       const double pos = position(p, row);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) angle(p, pos, c0 * 8 + e, c[e], s[e]);
+      for (int e = 0; e < 8; ++e) angle<FAR>(p, pos, c0 * 8 + e, c[e], s[e]);
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -143,6 +153,7 @@ __host__ __device__ inline int any_slots(int rot, int D) {
 }
 
 // Any even rot: one thread per (token, pair or copied columns, slice of heads).
+template <bool FAR>
 __global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p) {
   pdl_launch();
   pdl_wait();
@@ -153,7 +164,7 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p) {
   const int i = static_cast<int>(gid - row * per);
   const bool turns = 2 * i < p.rot, wide = 2 * i >= r8;
   float c = 1.f, s = 0.f;
-  if (turns) angle(p, position(p, row), i, c, s);
+  if (turns) angle<FAR>(p, position(p, row), i, c, s);
   const int ua = turns && !p.interleaved ? i : wide ? r8 + 8 * (i - r8 / 2) : 2 * i;
   const int ub = turns && !p.interleaved ? i + p.rot / 2 : 2 * i + 1;
   const int h0 = blockIdx.y * p.heads_per_slice;
@@ -210,8 +221,11 @@ int launch_rope(const RopeArgs& a) {
   p.heads_per_slice = static_cast<int>((heads + slices - 1) / slices);
   const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>((heads + p.heads_per_slice - 1) / p.heads_per_slice));
-  if (launch_early(wide ? rope_kernel : rope_any_kernel, grid, 256, 0,
-                   static_cast<cudaStream_t>(a.stream), 1, p))
+  const long long far = 1LL << 31;
+  auto kernel = wide ? rope_kernel<false> : rope_any_kernel<false>;
+  if (!a.positions && (a.first < -far || a.first + a.N > far))
+    kernel = wide ? rope_kernel<true> : rope_any_kernel<true>;
+  if (launch_early(kernel, grid, 256, 0, static_cast<cudaStream_t>(a.stream), 1, p))
     return TM_ERR_CUDA;
   return count_launches(1);
 }
