@@ -136,7 +136,7 @@ struct WtBars {
   uint64_t s_full[kWtTiles], s_empty[kWtTiles];
   uint64_t l_full[kWtLse], l_empty[kWtLse];
   uint64_t x_full[2], x_empty[2];  // [A tile]: the sums above
-  uint64_t j_full, j_empty;        // a kv head's joined statistics
+  uint64_t j_full;                 // the joined statistics
   uint64_t mma_done;
   uint32_t tmem;
   int abort_flag;
@@ -218,8 +218,8 @@ __device__ __forceinline__ bool wt_there(const WtParams& p, int len, int x) {
 }
 
 // JOIN (pass 2): the statistics of a kv head's rows are joined from pass 1's parts by
-// the reducing warps, into the memory of the lse slots; at most kWtLse q tiles. Without
-// it weights_lse_kernel does so in between.
+// the reducing warps, into the memory of the lse slots; at most kWtLse q tiles, and one
+// item a CTA. Without it weights_lse_kernel does so in between.
 template <int D, int PASS, bool JOIN = false>
 __global__ void __launch_bounds__(kWtThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       mbar_init(&bars->x_empty[i], 4);
     }
     mbar_init(&bars->j_full, 4 * kWtTiles);
-    mbar_init(&bars->j_empty, 4 * kWtTiles);
     mbar_init(&bars->mma_done, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -388,8 +387,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const Quintic kq = quintic();
     const F2 sl2 = both(p.sl2);
     uint32_t bc = 0, sc = 0, xc = 0;  // B tiles of the CTA, scores and items of this warpgroup
-    uint32_t jc = 0;  // kv heads joined, and the last of them
-    int joined = -1;
     const int phases = kWtTiles / p.group, ai = wg & (p.group - 1), phase = wg / p.group;
     bool ok = true;
     // another's B tile: only let its lse slot go
@@ -404,18 +401,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
       WtItem it;
       if (!wt_item<PASS>(p, i, it)) continue;
-      if (PASS == 2 && JOIN && it.b * p.Hkv + it.g != joined) {
-        // This kv head's statistics, in place of the slots: all 16 warps have left the head
-        // before, and each joins some rows of this one.
-        if (joined >= 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->j_empty);
-          ok = __all_sync(0xffffffffu, wait_bar(&bars->j_empty, (jc & 1) ^ 1, abort_flag, kSiteWeights));
-          if (!ok) break;
-        }
-        joined = it.b * p.Hkv + it.g;
+      if (PASS == 2 && JOIN) {
+        // The item's (the CTA's only one's) kv head: each of the 16 warps joins some of its rows.
         const long long per = static_cast<long long>(p.nqt) * 128;
-        const float2* st = p.stats + static_cast<long long>(joined) * p.parts * per;
+        const float2* st = p.stats + (static_cast<long long>(it.b) * p.Hkv + it.g) * p.parts * per;
         float* table = reinterpret_cast<float*>(smem + C::kLse);
         for (int x = tid; x < p.nqt * 128; x += 128 * kWtTiles) {
           float m, l;
@@ -424,9 +413,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->j_full);
-        ok = __all_sync(0xffffffffu, wait_bar(&bars->j_full, jc & 1, abort_flag, kSiteWeights));
+        ok = __all_sync(0xffffffffu, wait_bar(&bars->j_full, 0, abort_flag, kSiteWeights));
         if (!ok) break;
-        ++jc;
       }
       if (ai >= it.na) {  // no A tile for this warpgroup
         for (int t = it.t0; PASS == 2 && t < it.t1 && ok; ++t, ++bc) ok = pass_over(bc);
