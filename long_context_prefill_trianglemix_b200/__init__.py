@@ -373,9 +373,10 @@ def tm_debug_inject_stall(q, k, v, o, B, Hq, Hkv, N, D, scale, S, W, L, stream=N
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, Hkv, N, D, scale, S, W, L, _stream(stream)))
 
 
-def _device_ptrs(*xs):
+def _device_ptrs(*xs, strided=0):
     """Addresses of the arguments; a tensor has to lie on the current device (a kernel that
-    reads another device's or the host's memory faults)."""
+    reads another device's or the host's memory faults), and, but for the first ``strided``
+    ones, to be contiguous (the library would read the rows between a slice's)."""
     out, here = [], None
     for x in xs:
         if x is None:
@@ -390,6 +391,9 @@ def _device_ptrs(*xs):
             if here is not None or device < 0 or device != (_device or _find_current_stream())():
                 raise ValueError(f"a tensor on {x.device}, which is not the current CUDA device")
             here = device
+        if len(out) >= strided and not x.is_contiguous():
+            raise ValueError(f"a tensor of shape {tuple(x.shape)} and strides {x.stride()} is not "
+                             "contiguous")
         out.append(x.data_ptr())
     return out
 
@@ -425,7 +429,7 @@ def tm_rope_fwd(q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_
     q_out_stride = _rows_apart(q_out, "q_out", B, N, q_out_stride)
     k_stride = _rows_apart(k, "k", B, N, k_stride)
     k_out_stride = _rows_apart(k_out, "k_out", B, N, k_out_stride)
-    q, q_out, k, k_out, f, pos = _device_ptrs(q, q_out, k, k_out, inv_freq, positions)
+    q, q_out, k, k_out, f, pos = _device_ptrs(q, q_out, k, k_out, inv_freq, positions, strided=4)
     return _check("tm_rope_fwd", lib().tm_rope_fwd(
         q, q_out, k, k_out, B, N, Hq, Hkv, D, q_stride, q_out_stride, k_stride, k_out_stride, rot,
         layout, int(inverse), f, mscale, pos, first, _stream(stream)))
@@ -448,7 +452,7 @@ def tm_kv8_append(k, v, k_stride, v_stride, B, n_src, n, Hkv, D, counts, index, 
     k_stride = _rows_apart(k, "k", B, n_src, k_stride)
     v_stride = _rows_apart(v, "v", B, n_src, v_stride)
     k, v, counts, index, lens, table, k8, v8, k_range, v_range = _device_ptrs(
-        k, v, counts, index, lens, table, k8, v8, k_range, v_range)
+        k, v, counts, index, lens, table, k8, v8, k_range, v_range, strided=2)
     return _check("tm_kv8_append", lib().tm_kv8_append(
         k, v, k_stride, v_stride, B, n_src, n, Hkv, D, counts, index, lens, table, max_pages, k8,
         v8, k_range, v_range, num_pages, page, format, _stream(stream)))

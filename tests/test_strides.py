@@ -15,7 +15,8 @@ def calls(monkeypatch):
             return lambda *args: made.append((name, args)) or tm.TM_OK
 
     monkeypatch.setattr(tm, "lib", lambda: Library())
-    monkeypatch.setattr(tm, "_device_ptrs", lambda *xs: [x if x is None else x.data_ptr() for x in xs])
+    monkeypatch.setattr(tm, "_device_ptrs",
+                        lambda *xs, **_: [x if x is None else x.data_ptr() for x in xs])
     monkeypatch.setattr(tm, "_stream", lambda s: 0)
     return made
 
@@ -94,3 +95,62 @@ def test_append_refuses_rows_that_are_elsewhere(calls):
         with pytest.raises(ValueError, match="apart"):
             bad()
     assert not calls
+
+
+class Slice:
+    """What the binding asks of a tensor on the current device, here of a host one."""
+
+    def __init__(self, x):
+        self.x = x
+
+    def get_device(self):
+        return 0
+
+    def __getattr__(self, name):
+        return getattr(self.x, name)
+
+
+def test_a_slice_that_no_stride_describes_is_refused(monkeypatch):
+    """One token's positions out of a longer table, some columns of a page table, q of one token
+    out of a packed projection: the library would read the rows between."""
+    import torch
+    made = []
+    monkeypatch.setattr(tm, "_device", lambda: 0)
+    monkeypatch.setattr(tm, "_stream", lambda s: 0)
+    library = type("Library", (), {"__getattr__": lambda self, name: lambda *a: made.append(name) or 0})()
+    monkeypatch.setattr(tm, "lib", lambda: library)
+    q, k, v = (Slice(t) for t in packed(3, 1, 4, 2, 64))
+    dense = [Slice(torch.zeros(t.x.shape, dtype=torch.bfloat16)) for t in (q, k)]
+    f = Slice(torch.zeros(32, dtype=torch.float64))
+    wide = torch.zeros((3, 8), dtype=torch.int32)
+    i32, page = Slice(torch.zeros(3, dtype=torch.int32)), Slice(torch.zeros((4, 2, 16, 64), dtype=torch.int8))
+    r, w = Slice(torch.zeros((4, 2))), Slice(torch.zeros((3, 2, 64)))
+
+    def rope(positions):
+        tm.tm_rope_fwd(q, dense[0], k, dense[1], 3, 1, 4, 2, 64, 512, 256, 512, 128, 64, 0, 0, f, 1.0,
+                       positions, 0)
+
+    def append(table):
+        tm.tm_kv8_append(k, v, 512, 512, 3, 1, 1, 2, 64, None, None, i32, table, 4, page, page, r, r, 4,
+                         16, 0)
+
+    def attend(q, table):
+        tm.tm_kv8_attn_fwd(q, dense[0], 3, 1, 4, 2, 64, 0.125, page, page, r, r, 4, 16, 0, table, 4, i32,
+                           None, 0, 0, w, 1024)
+
+    def select(weights):
+        tm.tm_kv_select(weights, 32, None, 3, 2, 32, 4, 0, 0, w, None)
+
+    few = Slice(wide[:, :4].contiguous())
+    rope(Slice(wide[:, :1].contiguous()))
+    append(few)
+    attend(dense[0], few)
+    select(Slice(w.x[..., :32].contiguous()))
+    assert made == ["tm_rope_fwd", "tm_kv8_append", "tm_kv8_attn_fwd", "tm_kv_select"]
+    for bad in [lambda: rope(Slice(wide[:, 2:3])), lambda: append(Slice(wide[:, :4])),
+                lambda: attend(dense[0], Slice(wide[:, :4])), lambda: attend(q, few),
+                lambda: select(Slice(w.x[..., :32])),
+                lambda: tm.tm_key_weights_fwd(q, dense[1], 3, 4, 2, 1, 64, 0.125, 1, None, w, 64, 0, w, 1024)]:
+        with pytest.raises(ValueError, match="contiguous"):
+            bad()
+    assert len(made) == 4
