@@ -1682,7 +1682,9 @@ struct WtLayout {
   long long lse, total;
 };
 // Time of nb B tiles against g A tiles (us, measured): rounds of four (B tile, A tile)
-// products for the four warpgroups, the last one by how many it occupies.
+// products for the four warpgroups, the last one by how many it occupies. One table for
+// both head sizes: exponentials bound a round, not products (131072 keys of 32 q and 8
+// kv heads take 562 us at D = 128 and 552 at D = 64).
 double weights_time(int g, int nb) {
   const double t[5] = {0.0, 0.95, 1.3, 1.8, 2.3};
   const int phases = kWtTiles / g;
@@ -1690,8 +1692,10 @@ double weights_time(int g, int nb) {
 }
 
 // The A tiles an item takes and the parts that the B tiles are cut into (1 in pass 2)
-// for the shortest run of `bg` x `a_tiles` x `b_tiles` on 148 SMs, by that time, a
-// fixed cost an item, and the waves of items.
+// for the shortest run of `bg` x `a_tiles` x `b_tiles` on a B200's 148 SMs, by that time,
+// a fixed cost an item, and the waves of items. (A constant: the parts decide the
+// workspace, whose size is asked for without a device. Sequences count as N long, since
+// lens is on the device: items past a shorter one's end leave their CTAs idle.)
 void weights_shape(long long bg, int a_tiles, int b_tiles, bool cut, int* group, int* splits) {
   double best = 1e300;
   for (int g = 1; g <= kWtTiles; g *= 2) {

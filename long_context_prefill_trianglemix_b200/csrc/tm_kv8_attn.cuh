@@ -145,8 +145,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& first, uint32_t& sec
 // need registers or shared memory that one row tile of D = 128 has a better use for:
 // 16 warps an SM with one tile each took 338 us where 12 with two took 350 (8 sequences
 // of 131072 tokens, e4m3). Under a sustained load the power cap brings the clock to
-// 1.5 to 1.6 GHz, where the conversions of int8 bound this kernel (378 us, 5.7 TB/s;
-// e4m3 338 us, 6.4 TB/s) and memory does not; in short runs both take 320 us (6.7 TB/s).
+// 1.5 to 1.6 GHz, where the conversions of int8 bound this kernel (340 to 378 us by what
+// the box's cap leaves, 6.3 to 5.7 TB/s; e4m3 338 us, 6.4 TB/s) and memory does not; in
+// short runs both take 320 us (6.7 TB/s).
 // Each warp has a ring of S units (K rows, then V rows, 128-byte swizzled by the TMA
 // load): one unit loads while another is computed; more in flight is slower (three deep
 // 347 us, two deep 324 in short runs).

@@ -152,7 +152,9 @@ __host__ __device__ inline int any_slots(int rot, int D) {
   return r8 / 2 + (D - r8) / 8;
 }
 
-// Any even rot: one thread per (token, pair or copied columns, slice of heads).
+// Any even rot: one thread per (token, pair or copied columns, slice of heads). The
+// 2-byte loads and stores of the turned columns bound it: 2 x 4173 tokens of 28 + 4
+// heads of 64 take 22, 27 and 36 us at rot 6, 24 and 40, rope_kernel 14 to 16 at 32.
 template <bool FAR>
 __global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p) {
   pdl_launch();

@@ -15,7 +15,9 @@
 // come from ballots and one scan over the warps; each pass has its own
 // histogram, so a pass costs one cluster barrier. 8 rows of 131072 weights: 12.7 us
 // (14.9 where all lie in a few bins); 128 rows of 8192: 6.7 to 7.8. Clusters of 16 do
-// not all fit at once: 35 us for the 8 rows.
+// not all fit at once: 35 us for the 8 rows. Many long rows have a CTA each, whose part
+// above 16384 weights is read again by every pass: 128 rows of 32768 take 25 us, of
+// 131072 77 us (67 MB, 10 us to read once).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -21,14 +21,18 @@
 // scores to registers in halves, so the next MMA into its buffer runs while it
 // reduces the second half and the other warpgroups work. A q tile packs
 // floor(128 / G) tokens of all G q heads of the group, so short L wastes no rows.
+// Where G does not divide 128 the rest of a q tile is no row: pass 2 then goes through
+// every tile with bounds, as through the diagonal and the last tile, because zeros in
+// its place would turn an infinite key into NaN.
 //
 // Bound: one exponential per score and pass. At 16 MUFU results a clock and SM a
 // 128 x 128 tile takes 1024 clocks, twice its MMA time, so 2 of 8 exponentials
 // run on the FMA pipe (ex2x2_quintic). Four warpgroups rather than two hide the
 // dependent-issue latency of the reductions. Measured: 131072 keys, the last 256
 // queries, 32 q and 8 kv heads, D = 128: 560 us (2 x 275 GFLOP, 0.98 PFLOP/s; 1.07 G
-// exponentials a pass, 231 us of MUFU alone at 1965 MHz), 665 us under the power
-// cap of a long run.
+// exponentials a pass, 231 us of MUFU alone at 1965 MHz), 625 to 670 us under the
+// power cap of a long run. 28 q and 4 kv heads (bounds, all exponentials on MUFU in
+// pass 2) 672 us where 32 and 4 take 550.
 
 constexpr int kWtTiles = 4;  // A tiles, reduction warpgroups
 constexpr int kWtThreads = 128 * kWtTiles + 64;
