@@ -408,7 +408,7 @@ def _rows_apart(x, name, B, N, stride):
     except AttributeError:
         return stride  # an address, or nothing
     if N == 1:
-        if stride == own[0] or B == 1:
+        if B == 1 or not own or stride == own[0]:
             return stride
         shape = x.shape
         if len(own) < 3 or shape[0] != B or shape[1] != 1:

@@ -58,6 +58,16 @@ def test_rope_of_several_tokens_passes_its_numbers_on(calls):
     assert [(args[9], args[11]) for _, args in calls] == [(512, 512)] * 2
 
 
+def test_rope_takes_a_buffer_of_another_shape_as_the_numbers_say(calls):
+    """The first element of the rows, or the buffer that holds them."""
+    import torch
+    x = torch.zeros(3 * 512, dtype=torch.bfloat16)
+    f = torch.zeros(32, dtype=torch.float64)
+    for q, k in ((x, x[256:]), (x[0], x[256]), (x.view(3, 512), x.view(3, 512)[:, 256:])):
+        tm.tm_rope_fwd(q, q, k, k, 3, 1, 4, 2, 64, 512, 512, 512, 512, 64, 0, 0, f, 1.0, None, 0)
+    assert all(args[0] == x.data_ptr() and args[9:13] == (512,) * 4 for _, args in calls) and len(calls) == 3
+
+
 def test_rope_refuses_rows_that_are_elsewhere(calls):
     q, k, _ = packed(3, 5, 4, 2, 64)
     for bad in [lambda: rope(q, k, 256, 512), lambda: rope(q, k, 512, 1024),
